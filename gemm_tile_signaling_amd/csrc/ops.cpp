@@ -1,0 +1,69 @@
+// Enqueue calls of the 4-bit operators and the mixture-of-experts layer
+// (include/fo_ops.h): argument checks on the host, then the launchers.
+#include <atomic>
+#include <cstdint>
+
+#include "ops_internal.h"
+
+namespace {
+
+bool aligned(const void *ptr, uintptr_t to) { return ptr && (reinterpret_cast<uintptr_t>(ptr) & (to - 1)) == 0; }
+
+bool is_16bit(int32_t dtype) { return dtype == FO_BF16 || dtype == FO_FP16; }
+
+// FO_OK if the current device runs the kernels.  The answer of each device is
+// kept: asking the runtime for a device's name takes longer than a small call.
+int device_status() {
+  constexpr int kDevices = 64;
+  static std::atomic<int8_t> known[kDevices];  // 0: not asked yet, 1: gfx950, -1: another
+  int dev = -1;
+  if (hipGetDevice(&dev) != hipSuccess) return FO_ERR_HIP;
+  int8_t k = dev >= 0 && dev < kDevices ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (k == 0) {
+    hipDeviceProp_t prop;
+    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return FO_ERR_HIP;
+    k = fo_arch_supported(prop.gcnArchName) ? 1 : -1;
+    if (dev >= 0 && dev < kDevices) known[dev].store(k, std::memory_order_relaxed);
+  }
+  return k > 0 ? FO_OK : FO_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fo_mx4_quantize(const void *x, int64_t rows, int64_t cols, int64_t ld, int32_t dtype, void *codes, void *scales,
+                    hipStream_t stream) {
+  if (rows < 0 || cols < 1 || ld < cols || !is_16bit(dtype)) return FO_ERR_INVALID;
+  if (rows == 0) return FO_OK;
+  if (!aligned(x, 2) || !aligned(codes, 16) || !aligned(scales, 16)) return FO_ERR_INVALID;
+  if (rows > (1ll << 40) || ld > (1ll << 40) / rows) return FO_ERR_UNSUPPORTED;
+  if (const int rc = device_status()) return rc;
+  return fo::launch_mx4_quantize(x, rows, cols, ld, dtype, codes, scales, stream);
+}
+
+int fo_mx4_dequantize(const void *codes, const void *scales, int64_t rows, int64_t cols, int32_t out_type, void *out,
+                      hipStream_t stream) {
+  if (rows < 0 || cols < 1 || !(is_16bit(out_type) || out_type == FO_FP32)) return FO_ERR_INVALID;
+  if (rows == 0) return FO_OK;
+  if (!aligned(codes, 16) || !aligned(scales, 16) || !aligned(out, out_type == FO_FP32 ? 4 : 2)) return FO_ERR_INVALID;
+  if (rows > (1ll << 40) || cols > (1ll << 40) / rows) return FO_ERR_UNSUPPORTED;
+  if (const int rc = device_status()) return rc;
+  return fo::launch_mx4_dequantize(codes, scales, rows, cols, out_type, out, stream);
+}
+
+int fo_mx4_gemm(const void *a_codes, const void *a_scales, const void *b_codes, const void *b_scales, void *out,
+                int64_t M, int64_t N, int64_t K, int32_t dtype, int32_t problems, const int32_t *row_ends,
+                hipStream_t stream) {
+  if (M < 0 || N < 1 || K < 1 || N % 8 || K % 32 || !is_16bit(dtype)) return FO_ERR_INVALID;
+  if (problems < 1 || (row_ends ? !aligned(row_ends, 4) : problems != 1)) return FO_ERR_INVALID;
+  if (problems > 4096 || M >= (1 << 30) || N >= (1 << 30) || K >= (1 << 22)) return FO_ERR_UNSUPPORTED;
+  if (M == 0) return FO_OK;
+  if (!aligned(a_codes, 16) || !aligned(a_scales, 16) || !aligned(b_codes, 16) || !aligned(b_scales, 16) ||
+      !aligned(out, 16))
+    return FO_ERR_INVALID;
+  if (const int rc = device_status()) return rc;
+  return fo::launch_mx4_gemm(a_codes, a_scales, b_codes, b_scales, out, M, N, K, dtype, problems, row_ends, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,79 @@
+/*
+ * fo_ops.h -- operators next to the signaling GEMM: 4-bit (MX) operands and
+ * their product, and a mixture-of-experts layer for a few tokens (gfx950).
+ *
+ * The conventions of fo.h hold here: every call returns a fo_status and throws
+ * nothing; the caller owns every buffer; enqueue calls are asynchronous on the
+ * given stream, neither allocate nor synchronise, check their arguments on the
+ * host before any launch, and need the buffers and the stream to belong to the
+ * current device, which must be gfx950 (FO_ERR_UNSUPPORTED otherwise).  Null or
+ * misaligned pointers, negative sizes and unknown enumerators are
+ * FO_ERR_INVALID.  A call with no rows (no tokens) enqueues nothing.
+ *
+ * The 4-bit format (OCP Microscaling, MXFP4).  32 consecutive values of a row
+ * form a block, held as 32 four-bit codes and one scale byte; a row of `cols`
+ * values has nb = ceil(cols / 32) blocks, the last one filled up with zeros.
+ *   code    sign bit and 3 bits for 0, 0.5, 1, 1.5, 2, 3, 4, 6 (E2M1)
+ *   scale   2^(byte - 127) (E8M0); 255: every value of the block is NaN
+ *   codes   uint8[rows][16 * nb]: value 2i of a row in the low half of byte i,
+ *           value 2i + 1 in the high half
+ *   scales  uint8[ceil(nb / 8)][rows][8]: block b of a row at [b / 8][row][b % 8],
+ *           so that the scales of one 256-value slice of consecutive rows are
+ *           contiguous.  Bytes past a row's last block are written as 0 and
+ *           their value is never used.
+ * Codes and scales are 16-byte aligned.
+ */
+#ifndef FO_OPS_H_
+#define FO_OPS_H_
+
+#include "fo.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Output types beyond fo_dtype. */
+#define FO_FP32 2
+
+/*
+ * x [rows][cols] (bf16 or fp16, row stride `ld` >= cols elements) -> codes, scales.
+ *   byte = max(0, E - 2), E the exponent field (as fp32) of the block's largest
+ *          magnitude, i.e. the scale is 2^(floor(log2 max|x|) - 2);
+ *   code = x / scale rounded to the nearest code value, ties to the even code,
+ *          magnitudes above 6 held as 6 (exact: the only rounding there is).
+ * A block that holds a NaN or an infinity gets byte 255 and zero codes.
+ * x: 2-byte aligned; rows >= 0, cols >= 1.
+ */
+int fo_mx4_quantize(const void *x, int64_t rows, int64_t cols, int64_t ld, int32_t dtype, void *codes, void *scales,
+                    hipStream_t stream);
+
+/*
+ * The values that codes and scales stand for, as out [rows][cols], contiguous.
+ * out_type: FO_BF16, FO_FP16 or FO_FP32 (fp32 holds every value exactly, bf16
+ * every value of at least 2^-126; fp16 rounds to nearest even, infinite past
+ * its range).  out: aligned to its element.
+ */
+int fo_mx4_dequantize(const void *codes, const void *scales, int64_t rows, int64_t cols, int32_t out_type, void *out,
+                      hipStream_t stream);
+
+/*
+ * out[m][n] = round(sum_k A[m][k] * B[p(m) * N + n][k]): the product of two 4-bit
+ * operands, A of M rows and B of problems * N rows, K values each (K % 32 == 0,
+ * K < 2^22).  Products are exact, sums are fp32, one rounding to dtype (nearest
+ * even).  out: dtype, [M][N] contiguous, N % 8 == 0.
+ *   row_ends  NULL: one problem, every row; otherwise device int32[problems], not
+ *             decreasing: problem p multiplies rows [row_ends[p-1], row_ends[p])
+ *             of A (from 0 for p = 0), which may be none.  Read on the device;
+ *             values outside [0, M] are taken as the nearest bound.  Rows from
+ *             row_ends[problems - 1] on are not written.
+ * 1 <= problems <= 4096; M, N < 2^30.
+ */
+int fo_mx4_gemm(const void *a_codes, const void *a_scales, const void *b_codes, const void *b_scales, void *out,
+                int64_t M, int64_t N, int64_t K, int32_t dtype, int32_t problems, const int32_t *row_ends,
+                hipStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* FO_OPS_H_ */

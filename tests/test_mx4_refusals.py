@@ -1,0 +1,92 @@
+"""Arguments that the 4-bit operators refuse, with the documented codes -- all without a GPU."""
+
+import ctypes
+import os
+import re
+
+import pytest
+
+fo = pytest.importorskip("gemm_tile_signaling_amd")
+torch = pytest.importorskip("torch")
+from gemm_tile_signaling_amd import mx4  # noqa: E402
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+INVALID, UNSUPPORTED = fo.FO_ERR_INVALID, fo.FO_ERR_UNSUPPORTED
+
+
+def test_every_declared_symbol_is_exported():
+    src = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "fo_ops.h")).read(), flags=re.S)
+    names = set(re.findall(r"\b(fo_[a-z0-9_]+)\s*\(", src))
+    assert {"fo_mx4_quantize", "fo_mx4_dequantize", "fo_mx4_gemm"} <= names
+    L = ctypes.CDLL(fo.LIB_PATH)
+    for n in names:
+        assert hasattr(L, n), n
+
+
+@pytest.mark.parametrize("args, code", [
+    ((16, -1, 32, 32, 0, 16, 16), INVALID),             # rows
+    ((16, 4, 0, 32, 0, 16, 16), INVALID),               # cols
+    ((16, 4, 32, 31, 0, 16, 16), INVALID),              # rows overlap
+    ((16, 4, 32, 32, 2, 16, 16), INVALID),              # fp32 is no input type
+    ((0, 4, 32, 32, 0, 16, 16), INVALID),               # null
+    ((17, 4, 32, 32, 0, 16, 16), INVALID),              # x not on an element
+    ((16, 4, 32, 32, 0, 24, 16), INVALID),              # codes misaligned
+    ((16, 4, 32, 32, 0, 16, 8), INVALID),               # scales misaligned
+    ((16, 1 << 41, 32, 32, 0, 16, 16), UNSUPPORTED),    # sizes past the index arithmetic
+    ((16, 1 << 20, 32, 1 << 30, 0, 16, 16), UNSUPPORTED),
+    ((0, 0, 32, 32, 0, 0, 0), 0),                       # no rows: nothing to do
+])
+def test_quantize(args, code):
+    assert mx4._ops().fo_mx4_quantize(*args, None) == code
+
+
+@pytest.mark.parametrize("args, code", [
+    ((16, 16, -1, 32, 0, 16), INVALID),
+    ((16, 16, 4, 0, 0, 16), INVALID),
+    ((16, 16, 4, 32, 3, 16), INVALID),
+    ((8, 16, 4, 32, 0, 16), INVALID),
+    ((16, 0, 4, 32, 0, 16), INVALID),
+    ((16, 16, 4, 32, 2, 18), INVALID),                  # fp32 output on half an element
+    ((16, 16, 1 << 30, 1 << 30, 2, 16), UNSUPPORTED),
+    ((0, 0, 0, 32, 2, 0), 0),
+])
+def test_dequantize(args, code):
+    assert mx4._ops().fo_mx4_dequantize(*args, None) == code
+
+
+GEMM = dict(a=16, sa=16, b=16, sb=16, out=16, M=4, N=8, K=32, dtype=0, problems=1, ends=0)
+
+
+@pytest.mark.parametrize("change, code", [
+    (dict(M=-1), INVALID), (dict(N=0), INVALID), (dict(N=12), INVALID), (dict(K=0), INVALID), (dict(K=48), INVALID),
+    (dict(dtype=2), INVALID), (dict(problems=0), INVALID), (dict(problems=2), INVALID), (dict(ends=6), INVALID),
+    (dict(a=0), INVALID), (dict(sa=8), INVALID), (dict(b=24), INVALID), (dict(sb=0), INVALID), (dict(out=8), INVALID),
+    (dict(M=1 << 30), UNSUPPORTED), (dict(N=1 << 30), UNSUPPORTED), (dict(K=1 << 22), UNSUPPORTED),
+    (dict(problems=4097, ends=16), UNSUPPORTED), (dict(M=0, a=0, out=0), 0),
+])
+def test_gemm(change, code):
+    assert mx4._ops().fo_mx4_gemm(*dict(GEMM, **change).values(), None) == code
+
+
+def test_host_tensors_and_shapes():
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="device tensor"):
+        fo.mx4_quantize(x)
+    with pytest.raises(ValueError, match="bfloat16 or float16"):
+        fo.mx4_quantize(x.float())
+    with pytest.raises(ValueError, match="bfloat16 or float16"):
+        fo.mx4_quantize(x.view(torch.int16))                  # 16 bits of an unnamed type
+    with pytest.raises(ValueError, match="rows, cols"):
+        fo.mx4_quantize(x[0])
+    with pytest.raises(ValueError, match="strides"):
+        fo.mx4_quantize(x.t())
+    with pytest.raises(ValueError, match="strides"):
+        fo.mx4_quantize(x[:1].expand(4, 64))
+    c, s = (torch.zeros(sh, dtype=torch.uint8) for sh in fo.mx4_shapes(4, 64))
+    with pytest.raises(ValueError, match="dtype"):
+        fo.mx4_dequantize(c, s, 64, dtype="fp8")
+    with pytest.raises(ValueError, match="device tensor"):
+        fo.mx4_dequantize(c, s, 64)
+    with pytest.raises(ValueError, match="device tensor"):
+        fo.mx4_gemm(c, s, c, s)
+    assert fo.mx4_shapes(3, 257) == ((3, 144), (2, 3, 8))
