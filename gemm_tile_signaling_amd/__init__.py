@@ -13,7 +13,8 @@ The names follow the C ABI in ``include/fo.h``: ``Plan`` wraps
 ``reorder_post_ep``, ``reorder_pre``, ``reorder_shards`` and ``row_exchange``
 wrap the enqueue calls of the same names, and ``search`` wraps
 ``fo_plan_search``.  The operators of ``include/fo_ops.h`` are ``mx4_quantize``,
-``mx4_dequantize`` and ``mx4_gemm`` (4-bit operands, ``mx4.py``).
+``mx4_dequantize`` and ``mx4_gemm`` (4-bit operands, ``mx4.py``) and ``Moe``, a
+mixture-of-experts layer for a few tokens (``moe.py``).
 """
 
 from __future__ import annotations
@@ -26,7 +27,8 @@ import numpy as np
 
 __all__ = ["Plan", "FoError", "lib", "LIB_PATH", "status_string", "stream_create", "stream_destroy",
            "arch_supported", "mfma_rate", "mfma_rate_flops", "FO_OK", "FO_ERR_INVALID", "FO_ERR_UNSUPPORTED", "FO_ERR_HIP", "FO_ERR_NOMEM",
-           "FO_ERR_TIMEOUT", "FO_ERR_STALE", "mx4_shapes", "mx4_quantize", "mx4_dequantize", "mx4_gemm"]
+           "FO_ERR_TIMEOUT", "FO_ERR_STALE", "mx4_shapes", "mx4_quantize", "mx4_dequantize", "mx4_gemm",
+           "Moe"]
 
 # FO_LIB names another build of the same library (the sanitizer build of the CPU tests)
 LIB_PATH = os.environ.get("FO_LIB") or os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfo.so")
@@ -414,3 +416,4 @@ class Plan:
 
 
 from .mx4 import mx4_dequantize, mx4_gemm, mx4_quantize, mx4_shapes  # noqa: E402  (needs the names above)
+from .moe import Moe  # noqa: E402

@@ -28,6 +28,19 @@ int device_status() {
   return k > 0 ? FO_OK : FO_ERR_UNSUPPORTED;
 }
 
+int moe_desc_status(const fo_moe_desc *d) {
+  if (!d || !is_16bit(d->dtype) || (d->weights != FO_MOE_16BIT && d->weights != FO_MOE_MX4)) return FO_ERR_INVALID;
+  if (d->renormalize != 0 && d->renormalize != 1) return FO_ERR_INVALID;
+  const int64_t unit = d->weights == FO_MOE_MX4 ? 32 : 8;
+  if (d->hidden < 1 || d->ffn < 1 || d->hidden % unit || d->ffn % unit) return FO_ERR_INVALID;
+  if (d->experts < 1 || d->top_k < 1 || d->top_k > d->experts || d->max_tokens < 1) return FO_ERR_INVALID;
+  if (d->first_expert < 0 || d->local_experts < 1 || d->local_experts > d->experts - d->first_expert)
+    return FO_ERR_INVALID;
+  if (d->hidden >= (1 << 20) || d->ffn >= (1 << 20) || d->experts > 1024 || d->top_k > 16 || d->max_tokens > 64)
+    return FO_ERR_UNSUPPORTED;
+  return FO_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -64,6 +77,32 @@ int fo_mx4_gemm(const void *a_codes, const void *a_scales, const void *b_codes, 
     return FO_ERR_INVALID;
   if (const int rc = device_status()) return rc;
   return fo::launch_mx4_gemm(a_codes, a_scales, b_codes, b_scales, out, M, N, K, dtype, problems, row_ends, stream);
+}
+
+int fo_moe_workspace_bytes(const fo_moe_desc *desc, int64_t *bytes) {
+  if (!bytes) return FO_ERR_INVALID;
+  if (const int rc = moe_desc_status(desc)) return rc;
+  *bytes = fo::moe_layout(*desc).bytes;
+  return FO_OK;
+}
+
+int fo_moe_forward(const fo_moe_desc *desc, int64_t tokens, const void *x, const void *router, const void *gate_up,
+                   const void *gate_up_scales, const void *down, const void *down_scales, void *out, int32_t *ids,
+                   float *weights, void *workspace, hipStream_t stream) {
+  if (const int rc = moe_desc_status(desc)) return rc;
+  if (tokens < 0) return FO_ERR_INVALID;
+  if (tokens > desc->max_tokens) return FO_ERR_UNSUPPORTED;
+  if (tokens == 0) return FO_OK;
+  if (!aligned(x, 16) || !aligned(router, 16) || !aligned(gate_up, 16) || !aligned(down, 16) || !aligned(out, 16) ||
+      !aligned(workspace, 256))
+    return FO_ERR_INVALID;
+  if (desc->weights == FO_MOE_MX4 ? !aligned(gate_up_scales, 16) || !aligned(down_scales, 16)
+                                  : gate_up_scales || down_scales)
+    return FO_ERR_INVALID;
+  if ((ids && !aligned(ids, 4)) || (weights && !aligned(weights, 4))) return FO_ERR_INVALID;
+  if (const int rc = device_status()) return rc;
+  return fo::launch_moe(*desc, (int32_t)tokens, x, router, gate_up, gate_up_scales, down, down_scales, out, ids,
+                        weights, workspace, stream);
 }
 
 }  // extern "C"

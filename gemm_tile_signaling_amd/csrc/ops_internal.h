@@ -17,4 +17,39 @@ int launch_mx4_gemm(const void *a_codes, const void *a_scales, const void *b_cod
                     int64_t M, int64_t N, int64_t K, int32_t dtype, int32_t problems, const int32_t *row_ends,
                     hipStream_t s);
 
+// Parts of a layer's workspace, as byte offsets; each begins on 256 bytes.
+struct MoeLayout {
+  int64_t counter;   // u32: router workgroups done; zero between calls
+  int64_t head;      // int32: number of active experts, then their local indices [local_experts]
+  int64_t masks;     // u64 [local_experts]: the tokens of each active expert
+  int64_t ids;       // int32 [max_tokens][top_k]: picked experts
+  int64_t wts;       // float [max_tokens][top_k]: their weights
+  int64_t logits;    // float [max_tokens][experts]
+  int64_t x_split;   // bf16 [2][max_tokens][hidden]: fp16 tokens as two bf16 values (4-bit weights only)
+  int64_t h;         // 16-bit [2][max_tokens * top_k][ffn]: the activations as pairs
+  int64_t bytes;
+};
+inline MoeLayout moe_layout(const fo_moe_desc &d) {
+  MoeLayout l{};
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  };
+  l.counter = take(4);
+  l.head = take(4 * (1 + (int64_t)d.local_experts));
+  l.masks = take(8 * (int64_t)d.local_experts);
+  l.ids = take(4 * (int64_t)d.max_tokens * d.top_k);
+  l.wts = take(4 * (int64_t)d.max_tokens * d.top_k);
+  l.logits = take(4 * (int64_t)d.max_tokens * d.experts);
+  l.x_split = take(d.weights == FO_MOE_MX4 && d.dtype == FO_FP16 ? 4 * d.max_tokens * d.hidden : 0);
+  l.h = take(4 * (int64_t)d.max_tokens * d.top_k * d.ffn);
+  l.bytes = at;
+  return l;
+}
+int launch_moe(const fo_moe_desc &d, int32_t tokens, const void *x, const void *router, const void *gate_up,
+               const void *gate_up_scales, const void *down, const void *down_scales, void *out, int32_t *ids,
+               float *weights, void *workspace, hipStream_t s);
+
 }  // namespace fo

@@ -1,0 +1,109 @@
+"""Mixture-of-experts layer for a few tokens (``fo_moe_forward`` in ``include/fo_ops.h``).
+
+``Moe`` describes a layer; it holds no tensors.  The caller keeps the weights
+and a workspace (``new_workspace``, zeroed once) and passes them to every
+``forward``; calls that may run at the same time need a workspace each.
+"""
+
+from __future__ import annotations
+
+import ctypes as C
+from typing import Optional
+
+from . import _DTYPES, _check, _stream
+from .mx4 import _current, _new, _on, _ops, mx4_shapes
+
+__all__ = ["Moe"]
+
+_WEIGHTS = {"16": 0, "mx4": 1}
+
+
+class _MoeDesc(C.Structure):
+    _fields_ = [("hidden", C.c_int64), ("ffn", C.c_int64), ("experts", C.c_int32), ("top_k", C.c_int32),
+                ("first_expert", C.c_int32), ("local_experts", C.c_int32), ("dtype", C.c_int32), ("weights", C.c_int32),
+                ("renormalize", C.c_int32), ("max_tokens", C.c_int32)]
+
+
+def _buffer(x, name: str, numel: int, itemsize: int, device) -> int:
+    """Address of a contiguous device tensor of this many elements (of any shape) of this size."""
+    if x.numel() != numel:
+        raise ValueError(f"{name}: {x.numel()} elements, expected {numel}")
+    if x.element_size() != itemsize:
+        raise ValueError(f"{name}: element size {x.element_size()} != {itemsize}")
+    if not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    _on(x, name, device)
+    return x.data_ptr()
+
+
+class Moe:
+    """Router, top-k, gated (SiLU) experts and the weighted sum, for at most ``max_tokens`` <= 64 tokens.
+
+    ``weights``: "16" (gate_up [local_experts, 2 * ffn, hidden] and down
+    [local_experts, hidden, ffn] in ``dtype``) or "mx4" (each the (codes,
+    scales) of its rows stacked, as ``mx4_quantize`` gives them).
+    ``first_expert``, ``local_experts``: the share of the experts held here
+    (default: all); the router still covers all of them.
+    """
+
+    def __init__(self, hidden: int, ffn: int, experts: int, top_k: int, *, dtype: str = "bf16", weights: str = "16",
+                 renormalize: bool = True, first_expert: int = 0, local_experts: Optional[int] = None,
+                 max_tokens: int = 64):
+        if dtype not in _DTYPES:
+            raise ValueError(f"dtype: {dtype!r}, expected one of {sorted(_DTYPES)}")
+        if weights not in _WEIGHTS:
+            raise ValueError(f"weights: {weights!r}, expected one of {sorted(_WEIGHTS)}")
+        self.hidden, self.ffn, self.experts, self.top_k = int(hidden), int(ffn), int(experts), int(top_k)
+        self.dtype, self.weights, self.renormalize = dtype, weights, bool(renormalize)
+        self.first_expert = int(first_expert)
+        self.local_experts = self.experts - self.first_expert if local_experts is None else int(local_experts)
+        self.max_tokens = int(max_tokens)
+        self._d = _MoeDesc(self.hidden, self.ffn, self.experts, self.top_k, self.first_expert, self.local_experts,
+                           _DTYPES[dtype], _WEIGHTS[weights], int(self.renormalize), self.max_tokens)
+        n = C.c_int64()
+        lib = _ops()
+        _check(lib.fo_moe_workspace_bytes(C.byref(self._d), C.byref(n)), "fo_moe_workspace_bytes")
+        self.workspace_bytes = n.value
+        self._ref = C.byref(self._d)
+
+    def new_workspace(self, device="cuda"):
+        """A zeroed workspace, uint8 [workspace_bytes]."""
+        import torch
+        return torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=device)
+
+    def _matrix(self, m, name: str, rows: int, cols: int, device):
+        """(address, address of the scales or 0) of one of the experts' matrices, its rows stacked."""
+        if self.weights == "16":
+            return _buffer(m, name, rows * cols, 2, device), 0
+        codes, scales = m
+        c, s = mx4_shapes(rows, cols)
+        return (_buffer(codes, name + " codes", c[0] * c[1], 1, device),
+                _buffer(scales, name + " scales", s[0] * s[1] * s[2], 1, device))
+
+    def forward(self, x, router, gate_up, down, workspace, out=None, picks=None, stream=None):
+        """out [tokens, hidden] of x [tokens, hidden] (``fo_moe_forward``).
+
+        ``picks``: optional (ids int32, weights float32), each [tokens, top_k],
+        that receive the picked experts and their weights."""
+        import torch
+        if x.dim() != 2 or x.shape[1] != self.hidden:
+            raise ValueError(f"x: shape {tuple(x.shape)}, expected [tokens, {self.hidden}]")
+        device, tokens = _current(x, "x"), x.shape[0]
+        if tokens > self.max_tokens:
+            raise ValueError(f"x: {tokens} tokens, the layer is for at most {self.max_tokens}")
+        wanted = torch.bfloat16 if self.dtype == "bf16" else torch.float16
+        if x.dtype not in (wanted, torch.int16):
+            raise ValueError(f"x: {x.dtype}, the layer computes in {self.dtype}")
+        if out is None:
+            out, = _new(stream, device, ((tokens, self.hidden), wanted))
+        n, L, D, F = tokens * self.top_k, self.local_experts, self.hidden, self.ffn
+        gu, gus = self._matrix(gate_up, "gate_up", L * 2 * F, D, device)
+        dn, dns = self._matrix(down, "down", L * D, F, device)
+        ids, wts = (0, 0) if picks is None else (_buffer(picks[0], "picked ids", n, 4, device),
+                                                 _buffer(picks[1], "picked weights", n, 4, device))
+        _check(_ops().fo_moe_forward(
+            self._ref, tokens, _buffer(x, "x", tokens * D, 2, device),
+            _buffer(router, "router", self.experts * D, 2, device), gu, gus, dn, dns,
+            _buffer(out, "out", tokens * D, 2, device), ids, wts,
+            _buffer(workspace, "workspace", self.workspace_bytes, 1, device), _stream(stream)), "fo_moe_forward")
+        return out

@@ -34,6 +34,8 @@ def _ops():
             "fo_mx4_quantize": [vp, i64, i64, i64, i32, vp, vp, vp],
             "fo_mx4_dequantize": [vp, vp, i64, i64, i32, vp, vp],
             "fo_mx4_gemm": [vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, vp, vp],
+            "fo_moe_workspace_bytes": [vp, vp],
+            "fo_moe_forward": [vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp],
         }.items():
             f = getattr(L, name)
             f.argtypes = args

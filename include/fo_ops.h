@@ -72,6 +72,63 @@ int fo_mx4_gemm(const void *a_codes, const void *a_scales, const void *b_codes, 
                 int64_t M, int64_t N, int64_t K, int32_t dtype, int32_t problems, const int32_t *row_ends,
                 hipStream_t stream);
 
+/* Storage of the experts' weights. */
+typedef enum fo_moe_weights {
+  FO_MOE_16BIT = 0,   /* the layer's dtype, row-major                      */
+  FO_MOE_MX4 = 1      /* codes and scales of the 4-bit format, rows stacked */
+} fo_moe_weights;
+
+/*
+ * A mixture-of-experts layer.  For each token x (hidden values):
+ *   l[e]   = router[e] . x                            over all `experts`, fp32
+ *   picks  = the top_k experts of largest l (ties: the lowest index; a NaN is
+ *            larger than every number)
+ *   w[j]   = softmax(l)[pick j], divided by the picks' sum if `renormalize`
+ *   h_e[f] = silu(gate_e[f] . x) * (up_e[f] . x)      silu(v) = v / (1 + exp(-v))
+ *   out    = sum over the picks e held here of w * (down_e . h_e)
+ * Experts [first_expert, first_expert + local_experts) are held here, the
+ * others elsewhere (expert parallelism: the shares' outputs add up); a token
+ * without a pick held here gives a row of zeros.
+ */
+typedef struct fo_moe_desc {
+  int64_t hidden, ffn;             /* positive multiples of 8 (16-bit weights) or 32 (4-bit); < 2^20 */
+  int32_t experts, top_k;          /* 1 <= top_k <= min(experts, 16); experts <= 1024               */
+  int32_t first_expert, local_experts;
+  int32_t dtype;                   /* fo_dtype of x, router, out and 16-bit weights                  */
+  int32_t weights;                 /* fo_moe_weights                                                 */
+  int32_t renormalize;             /* 0 or 1                                                         */
+  int32_t max_tokens;              /* 1 .. 64: the workspace is sized for it                         */
+} fo_moe_desc;
+
+/*
+ * Bytes of the workspace of a layer.  The caller zeroes the workspace once,
+ * before its first use; every call leaves it ready for the next.  Calls that
+ * may run at the same time need a workspace each.
+ */
+int fo_moe_workspace_bytes(const fo_moe_desc *desc, int64_t *bytes);
+
+/*
+ * The layer on tokens <= max_tokens rows of x: a few tokens, where reading the
+ * picked experts' weights once is the work (for more, sort the rows by expert
+ * and use the grouped products).
+ *   x        [tokens][hidden]
+ *   router   [experts][hidden]
+ *   gate_up  [local_experts][2 * ffn][hidden]: an expert's ffn gate rows, then its ffn up rows
+ *   down     [local_experts][hidden][ffn]
+ *            (4-bit: codes, with the scales of the stacked rows; NULL scales otherwise)
+ *   out      [tokens][hidden]
+ *   ids, weights  NULL, or [tokens][top_k]: the picks in descending order and their weights
+ * All 16-byte aligned (ids and weights 4), the workspace 256-byte aligned.
+ * Sums are fp32 and in a fixed order, so a call on the same inputs gives the
+ * same bits.  h is carried between the two products as a pair of 16-bit values
+ * (bf16 pairs hold 16 significant bits or more; fp16 pairs, used with fp16
+ * 16-bit weights, at least 21 from 2^-14 upwards, infinite past fp16's range).
+ * x in fp16 with 4-bit weights is split exactly into two bf16 values.
+ */
+int fo_moe_forward(const fo_moe_desc *desc, int64_t tokens, const void *x, const void *router, const void *gate_up,
+                   const void *gate_up_scales, const void *down, const void *down_scales, void *out, int32_t *ids,
+                   float *weights, void *workspace, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
