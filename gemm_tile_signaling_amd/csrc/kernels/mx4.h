@@ -36,6 +36,17 @@ __device__ __forceinline__ uint32_t mx4_pair(float lo, float hi, float scale) {
   return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, lo, hi, scale, 0) & 0xFFu;
 }
 
+template <typename T>
+__device__ __forceinline__ u32x2 pack4(f32x4 v);
+template <>
+__device__ __forceinline__ u32x2 pack4<__bf16>(f32x4 v) {
+  return __builtin_bit_cast(u32x2, __builtin_convertvector(v, bf16x4));
+}
+template <>
+__device__ __forceinline__ u32x2 pack4<_Float16>(f32x4 v) {
+  return __builtin_bit_cast(u32x2, __builtin_convertvector(v, f16x4));
+}
+
 // One scaled MFMA on 4-bit operands: lane l holds 32 values of row l % 32 (l % 16)
 // of each operand and their scale in byte SA (SB) of sa (sb).
 template <int SA, int SB>

@@ -1,5 +1,8 @@
 // Product of two 4-bit (MX) operands: out = A . B^T, sums in fp32.
+#include <type_traits>
+
 #include "../ops_internal.h"
+#include "buffer.h"
 #include "mx4.h"
 
 namespace fo {
@@ -12,6 +15,7 @@ struct Mx4Params {
   int32_t nb;               // blocks of a row
   int32_t problems;
   const int32_t *row_ends;  // NULL: one problem
+  int32_t row_tiles, col_tiles, swizzle, remap;
 };
 
 // Rows [begin, end) and problem of row tile i (tiles of BM rows, no tile spans
@@ -48,37 +52,331 @@ __device__ __forceinline__ bool find_rows(const Mx4Params &p, int BM, int64_t i,
   return false;
 }
 
-// One wave per 16 x 16 tile, operands straight from memory.
-template <typename T>
-__global__ __launch_bounds__(64) void mx4_gemm_simple(Mx4Params p) {
-  int problem;
-  int64_t row0, row_end;
-  const uint32_t tn = (uint32_t)((p.N + 15) / 16), tile_n = blockIdx.x % tn;
-  if (!find_rows(p, 16, blockIdx.x / tn, &problem, &row0, &row_end)) return;
-  const int lane = threadIdx.x, r = lane & 15, g = lane >> 4;
-  const int64_t m = row0 + r, n = (int64_t)tile_n * 16 + r, bn = problem * p.N + n;
-  const bool m_ok = m < row_end, n_ok = n < p.N;
-  f32x4 acc = {};
-  const int64_t b_rows = p.problems * p.N;
-  for (int k = g; k - g < p.nb; k += 4) {  // block k of the row
-    u32x4 a = {}, b = {};
-    uint32_t sa = 0, sb = 0;
-    if (m_ok && k < p.nb) {
-      a = *reinterpret_cast<const u32x4 *>(p.a + (m * p.nb + k) * 16);
-      sa = p.as[((k / 8) * p.M + m) * 8 + k % 8];
+typedef __attribute__((address_space(3))) void lds_void;
+
+// s_waitcnt immediate for vmcnt(n) with the other counters unconstrained (gfx9 encoding)
+constexpr int vmcnt_imm(int n) { return 0x0F70 | (n & 0xF) | ((n >> 4) << 14); }
+constexpr int kLgkmcntZero = 0xC07F;  // s_waitcnt lgkmcnt(0), other counters unconstrained
+
+// Workgroup barrier that does not wait for outstanding memory operations.
+__device__ __forceinline__ void bare_barrier() {
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_s_barrier();
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
+// Wait until at most min(s, S) slices of LOADS loads each, and EXTRA younger
+// operations, are in flight (s is wave-uniform; the waits need immediates).
+template <int LOADS, int S, int EXTRA = 0>
+__device__ __forceinline__ void wait_slices(int s) {
+  if constexpr (S > 0) {
+    if (s >= S) {
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm(S * LOADS + EXTRA));
+      return;
     }
-    if (n_ok && k < p.nb) {
-      b = *reinterpret_cast<const u32x4 *>(p.b + (bn * p.nb + k) * 16);
-      sb = p.bs[((k / 8) * b_rows + bn) * 8 + k % 8];
-    }
-    acc = mx4_mma16<0, 0>(b, sb, a, sa, acc);
+    wait_slices<LOADS, S - 1, EXTRA>(s);
+  } else {
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(EXTRA));
   }
-  // lane: columns 4 g .. 4 g + 3 of row r
-  if (m_ok)
-    for (int i = 0; i < 4; ++i) {
-      const int64_t c = (int64_t)tile_n * 16 + g * 4 + i;
-      if (c < p.N) reinterpret_cast<T *>(p.out)[m * p.N + c] = (T)acc[i];
+}
+
+template <int I, int N, typename F>
+__device__ __forceinline__ void static_for(F &&f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    static_for<I + 1, N>(f);
+  }
+}
+
+constexpr uint32_t kOutOfRange = 0xC0000000u;  // a byte offset past every buffer resource made here
+
+// Tile BM x BN; K-slices of 256 values (128 bytes of codes a row, 8 blocks) in
+// a ring of NS LDS stages; NW waves in a WGM x WGN grid.
+template <int BM, int BN, int NW, int NS_>
+struct Cfg {
+  static constexpr int THREADS = 64 * NW, NS = NS_, DIST = NS - 1;
+  static constexpr int WGM = 2, WGN = NW / 2;
+  static constexpr int WM = BM / WGM, WN = BN / WGN, FM = WM / 32, FN = WN / 32;
+  static constexpr int ROWB = 128, CHUNKS = 8, KS = 4;   // a slice is 4 k-steps of 64 values
+  static constexpr int A_PER_T = BM * CHUNKS / THREADS, B_PER_T = BN * CHUNKS / THREADS;
+  // scale bytes of a slice: 8 a row, loaded 4 a lane: 2 BM + 2 BN lanes
+  static constexpr int S_PER_T = (2 * BM + 2 * BN) / THREADS;
+  static constexpr int LOADS = A_PER_T + B_PER_T + S_PER_T;
+  static constexpr int DPB = NS == 2 ? LOADS : (LOADS + KS - 1) / KS;  // loads issued per k-step
+  static constexpr int B_AT = BM * ROWB, S_AT = (BM + BN) * ROWB, STAGE = S_AT + (BM + BN) * 8;
+  static constexpr int OUT_PITCH = 80;                   // a wave's 32 x 32 block: 64 bytes a row, padded
+  static constexpr int OUT_AT = NS * STAGE, LDS = OUT_AT + NW * 32 * OUT_PITCH;
+  static constexpr int STORES = FM * FN * 2;
+  static_assert(BM * CHUNKS % THREADS == 0 && BN * CHUNKS % THREADS == 0 && (S_PER_T == 1 || (S_PER_T == 2 && BM == BN)), "chunk split");
+  static_assert(DIST * LOADS + STORES <= 63, "operations in flight fit the vmcnt counter");
+  static_assert(LDS <= 160 * 1024, "LDS of one CU");
+};
+
+template <typename T, int BM, int BN, int NW, int NS_>
+__global__ __launch_bounds__(64 * NW, 2) void mx4_gemm_tiled(Mx4Params p) {
+  using C = Cfg<BM, BN, NW, NS_>;
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / C::WGN, wn = wave % C::WGN;
+  const uint32_t pitch = (uint32_t)p.nb * 16u;  // bytes of a row of codes
+  const int nk = (p.nb + 7) / 8, left = p.nb - (nk - 1) * 8;  // slices; blocks of the last one
+
+  // Codes to LDS: instruction q of wave w fills rows (NW q + w) * 8 .. + 8, lane l
+  // at physical chunk l % 8 of its row, which holds logical chunk
+  // (l % 8) ^ ((row / 2) % 8): the 16 rows that one LDS cycle serves then touch all banks.
+  const int dma_row = wave * 8 + lane / 8, dma_chunk = (lane % 8) ^ ((dma_row / 2) % 8);
+  const uint32_t g_base = (uint32_t)dma_row * pitch + (uint32_t)dma_chunk * 16u, g_step = (uint32_t)(NW * 8) * pitch;
+  // in the last slice the chunks past the row's end read zeros
+  const uint32_t g_last = dma_chunk < left ? g_base : kOutOfRange;
+
+  // Fragments: row lane % 32 of each 32-row block; the lane's half h takes logical
+  // chunks 4 h + s in k-step s, so that one dword holds its scales of the slice's 4 k-steps.
+  const int frag_row = lane & 31, half = lane >> 5, swz = (frag_row / 2) % 8;
+  const uint32_t a_frag = (uint32_t)((wm * C::WM + frag_row) * C::ROWB);
+  const uint32_t b_frag = (uint32_t)(C::B_AT + (wn * C::WN + frag_row) * C::ROWB);
+  const uint32_t a_sc = (uint32_t)(C::S_AT + (wm * C::WM + frag_row) * 8 + half * 4);
+  const uint32_t b_sc = (uint32_t)(C::S_AT + BM * 8 + (wn * C::WN + frag_row) * 8 + half * 4);
+  const int blocks_here = left - half * 4;  // of the lane's 4 blocks in the last slice
+  const uint32_t last_mask = blocks_here >= 4 ? 0xFFFFFFFFu : blocks_here <= 0 ? 0u : (1u << (8 * blocks_here)) - 1u;
+
+  int64_t row0 = 0, row_end = 0, col0 = 0, b_row0 = 0;
+  __amdgpu_buffer_rsrc_t ra = make_rsrc(p.a, 0), rb = make_rsrc(p.b, 0), rc = make_rsrc(p.out, 0);
+  const uint8_t *sa0 = p.as, *sb0 = p.bs;  // scales of the next slice to load
+  uint32_t rows = 0, cols = 0;
+
+  // Tile order: bands of SWIZZLE row tiles, column by column, so that tiles next
+  // to each other share operands; consecutive positions sit on one XCD.
+  const int64_t total = (int64_t)p.row_tiles * p.col_tiles;
+  auto load_tile = [&](int64_t i) {  // false: a position without rows
+    const int64_t per_band = (int64_t)p.swizzle * p.col_tiles, band = i / per_band, in = i - band * per_band;
+    const int32_t h = (int32_t)min((int64_t)p.swizzle, p.row_tiles - band * p.swizzle);
+    const int64_t tm = band * p.swizzle + in % h, tn = in / h;
+    int problem;
+    if (!find_rows(p, BM, tm, &problem, &row0, &row_end)) return false;
+    col0 = tn * BN;
+    rows = (uint32_t)min((int64_t)BM, row_end - row0);
+    cols = (uint32_t)min((int64_t)BN, p.N - col0);
+    b_row0 = (int64_t)problem * p.N + col0;
+    ra = make_rsrc(p.a + row0 * pitch, rows * pitch);
+    rb = make_rsrc(p.b + b_row0 * pitch, cols * pitch);
+    rc = make_rsrc(p.out + row0 * p.N + col0, (uint32_t)(((rows - 1) * p.N + cols) * 2));
+    sa0 = p.as + row0 * 8;
+    sb0 = p.bs + b_row0 * 8;
+    return true;
+  };
+  // instructions [q0, q1) of slice kt's loads into its stage
+  auto dma = [&](auto q0c, auto q1c, int kt) {
+    constexpr int q0 = decltype(q0c)::value, q1 = decltype(q1c)::value;
+    char *dst = smem + (kt % C::NS) * C::STAGE;
+    const uint32_t at = kt == nk - 1 ? g_last : g_base, soff = (uint32_t)kt * C::ROWB;
+    static_for<q0, q1>([&](auto qc) {
+      constexpr int q = decltype(qc)::value;
+      if constexpr (q < C::A_PER_T) {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void *)(dst + (q * NW + wave) * 1024), 16, at + q * g_step, soff, 0, 0);
+      } else if constexpr (q < C::A_PER_T + C::B_PER_T) {
+        constexpr int qb = q - C::A_PER_T;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void *)(dst + C::B_AT + (qb * NW + wave) * 1024), 16, at + qb * g_step,
+                                                 soff, 0, 0);
+      } else {
+        // pieces of 64 dwords (32 rows) of the scales: A's rows, then B's
+        constexpr int qs = q - C::A_PER_T - C::B_PER_T;
+        const int piece = qs * NW + wave;
+        const bool is_a = C::S_PER_T == 2 ? qs == 0 : wave < BM / 32;
+        const __amdgpu_buffer_rsrc_t rs = is_a ? make_rsrc(sa0, rows * 8) : make_rsrc(sb0, cols * 8);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(dst + C::S_AT + piece * 256), 4,
+                                                 (uint32_t)((is_a ? piece : piece - BM / 32) * 256 + lane * 4), 0, 0, 0);
+        if constexpr (q == C::LOADS - 1) {  // slices are loaded in order
+          sa0 += p.M * 8;
+          sb0 += (int64_t)p.problems * p.N * 8;
+        }
+      }
+    });
+  };
+  using std::integral_constant;
+  auto dma_part = [&](auto partc, int kt) {
+    constexpr int part = decltype(partc)::value;
+    constexpr int q0 = part * C::DPB < C::LOADS ? part * C::DPB : C::LOADS;
+    constexpr int q1 = q0 + C::DPB < C::LOADS ? q0 + C::DPB : C::LOADS;
+    dma(integral_constant<int, q0>{}, integral_constant<int, q1>{}, kt);
+  };
+  auto prologue = [&]() {  // slices 0 .. NS-2
+#pragma unroll
+    for (int kt = 0; kt < C::DIST; ++kt)
+      if (kt < nk) dma(integral_constant<int, 0>{}, integral_constant<int, C::LOADS>{}, kt);
+  };
+
+  const int64_t step = gridDim.x;
+  int64_t b = p.remap ? (int64_t)(blockIdx.x & 7) * (step >> 3) + (blockIdx.x >> 3) : blockIdx.x;
+  while (b < total && !load_tile(b)) b += step;
+  if (b >= total) return;
+  prologue();
+  bool first = true;
+  for (;;) {
+    f32x16 acc[C::FM][C::FN] = {};
+    u32x4 fa[2][C::FM], fb[2][C::FN];
+    uint32_t sa[C::FM], sb[C::FN];  // scales of the slice: byte s for k-step s
+    auto read_frags = [&](auto uc, int kt, int ks) {
+      constexpr int u = decltype(uc)::value;
+      const char *base = smem + (kt % C::NS) * C::STAGE;
+      const uint32_t chunk = (uint32_t)(((half * 4 + ks) ^ swz) << 4);
+#pragma unroll
+      for (int f = 0; f < C::FN; ++f) fb[u][f] = *reinterpret_cast<const u32x4 *>(base + b_frag + f * 32 * C::ROWB + chunk);
+#pragma unroll
+      for (int f = 0; f < C::FM; ++f) fa[u][f] = *reinterpret_cast<const u32x4 *>(base + a_frag + f * 32 * C::ROWB + chunk);
+    };
+    auto read_scales = [&](int kt, uint32_t(&ta)[C::FM], uint32_t(&tb)[C::FN]) {
+      const char *base = smem + (kt % C::NS) * C::STAGE;
+      const uint32_t mask = kt == nk - 1 ? last_mask : 0xFFFFFFFFu;
+#pragma unroll
+      for (int f = 0; f < C::FN; ++f) tb[f] = *reinterpret_cast<const uint32_t *>(base + b_sc + f * 256) & mask;
+#pragma unroll
+      for (int f = 0; f < C::FM; ++f) ta[f] = *reinterpret_cast<const uint32_t *>(base + a_sc + f * 256) & mask;
+    };
+    auto mfmas = [&](auto uc, auto sc) {
+      constexpr int u = decltype(uc)::value, ks = decltype(sc)::value;
+#pragma unroll
+      for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) acc[i][j] = mx4_mma32<ks, ks>(fb[u][j], sb[j], fa[u][i], sa[i], acc[i][j]);
+    };
+    // Order inside a k-step: its loads spread out, its LDS reads one to an MFMA
+    // from the start, so that they are back before the next step needs them.
+    constexpr int NR = C::FM + C::FN, NM = C::FM * C::FN;
+    auto order = [&](auto ndc, auto nrc) {
+      constexpr int ND = decltype(ndc)::value, R = decltype(nrc)::value;
+      static_for<0, R>([&](auto rc_) {
+        constexpr int r = decltype(rc_)::value;
+        if constexpr (r % 2 == 0 && r / 2 < ND) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // VMEM read
+        __builtin_amdgcn_sched_group_barrier(0x100, R > NM ? 2 : 1, 0);                               // DS read
+        if constexpr (r < NM) __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                     // MFMA
+      });
+      if constexpr ((R + 1) / 2 < ND) __builtin_amdgcn_sched_group_barrier(0x020, ND - (R + 1) / 2, 0);
+      if constexpr (NM > R) __builtin_amdgcn_sched_group_barrier(0x008, NM - R, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    // k-steps 0 .. 2 of a slice, each reading the next step's fragments, with the slice's share of loads
+    auto blocks = [&](int kt, auto dmac) {
+      __builtin_amdgcn_sched_barrier(0);
+      static_for<0, 3>([&](auto sc) {
+        constexpr int st = decltype(sc)::value;
+        if constexpr (decltype(dmac)::value) dma_part(sc, kt + C::DIST);
+        read_frags(integral_constant<int, (st + 1) % 2>{}, kt, st + 1);
+        mfmas(integral_constant<int, st % 2>{}, sc);
+        constexpr int left_q = C::LOADS - st * C::DPB;
+        order(integral_constant<int, decltype(dmac)::value ? (left_q < 0 ? 0 : left_q < C::DPB ? left_q : C::DPB) : 0>{},
+              integral_constant<int, NR>{});
+      });
+    };
+    // the last k-step, beside the first reads of the next slice (which has landed for every wave)
+    auto hand_over = [&](int kt) {
+      uint32_t ta[C::FM], tb[C::FN];
+      read_scales(kt + 1, ta, tb);
+      read_frags(integral_constant<int, 0>{}, kt + 1, 0);
+      mfmas(integral_constant<int, 1>{}, integral_constant<int, 3>{});
+      order(integral_constant<int, 0>{}, integral_constant<int, 2 * NR>{});
+#pragma unroll
+      for (int f = 0; f < C::FM; ++f) sa[f] = ta[f];
+#pragma unroll
+      for (int f = 0; f < C::FN; ++f) sb[f] = tb[f];
+    };
+    // slice 0 has landed once at most min(DIST - 1, nk - 1) slices, and the last tile's stores, are in flight
+    if (first)
+      wait_slices<C::LOADS, C::DIST - 1>(nk - 1);
+    else
+      wait_slices<C::LOADS, C::DIST - 1, C::STORES>(nk - 1);
+    first = false;
+    bare_barrier();
+    read_scales(0, sa, sb);
+    read_frags(integral_constant<int, 0>{}, 0, 0);
+    int kt = 0;
+    for (; kt + C::DIST < nk; ++kt) {
+      blocks(kt, std::true_type{});
+      dma_part(integral_constant<int, 3>{}, kt + C::DIST);
+      __builtin_amdgcn_s_waitcnt(kLgkmcntZero);  // this wave's reads of slice kt are complete
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm((C::DIST - 1) * C::LOADS));
+      bare_barrier();
+      hand_over(kt);
     }
+    if constexpr (C::DIST > 1)
+      for (; kt + 1 < nk; ++kt) {
+        blocks(kt, std::false_type{});
+        __builtin_amdgcn_s_waitcnt(kLgkmcntZero);
+        wait_slices<C::LOADS, C::DIST - 2>(nk - 2 - kt);
+        bare_barrier();
+        hand_over(kt);
+      }
+    blocks(nk - 1, std::false_type{});
+    mfmas(integral_constant<int, 1>{}, integral_constant<int, 3>{});
+    __builtin_amdgcn_sched_barrier(0);
+
+    // ---- next tile's first slices, before this tile's stores; every wave has read its last fragments
+    const uint32_t o_rows = rows, o_cols = cols;
+    const __amdgpu_buffer_rsrc_t o_rc = rc;
+    __builtin_amdgcn_s_waitcnt(kLgkmcntZero);
+    bare_barrier();
+    b += step;
+    while (b < total && !load_tile(b)) b += step;
+    const bool more = b < total;
+    if (more) prologue();
+
+    // ---- epilogue: a wave's 32 x 32 blocks through its own LDS piece to 16-byte stores.
+    // Lane: row lane % 32, columns 8 q + 4 half .. + 3 (q = 0 .. 3) of a block.
+    char *const out_w = smem + C::OUT_AT + wave * 32 * C::OUT_PITCH;
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x4 v = {acc[i][j][q * 4], acc[i][j][q * 4 + 1], acc[i][j][q * 4 + 2], acc[i][j][q * 4 + 3]};
+          *reinterpret_cast<u32x2 *>(out_w + frag_row * C::OUT_PITCH + q * 16 + half * 8) = pack4<T>(v);
+        }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const uint32_t r = s * 16 + lane / 4, c = lane % 4;
+          const u32x4 v = *reinterpret_cast<const u32x4 *>(out_w + r * C::OUT_PITCH + c * 16);
+          const uint32_t orow = wm * C::WM + i * 32 + r, ocol = wn * C::WN + j * 32 + c * 8;
+          const uint32_t off = orow < o_rows && ocol < o_cols ? (orow * (uint32_t)p.N + ocol) * 2u : kOutOfRange;
+          __builtin_amdgcn_raw_buffer_store_b128(v, o_rc, off, 0, 0);
+        }
+        __builtin_amdgcn_wave_barrier();
+      }
+    if (!more) return;
+  }
+}
+
+template <typename T, int BM, int BN, int NW, int NS>
+int launch_tiled(Mx4Params p, int cus, hipStream_t s) {
+  using C = Cfg<BM, BN, NW, NS>;
+  const void *fn = reinterpret_cast<const void *>(&mx4_gemm_tiled<T, BM, BN, NW, NS>);
+  static bool configured = false;  // per process; the attribute is per kernel and device-independent
+  if (!configured) {
+    if (hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS) != hipSuccess) return FO_ERR_HIP;
+    configured = true;
+  }
+  const int64_t row_tiles = p.row_ends ? (p.M + (int64_t)p.problems * (BM - 1)) / BM : (p.M + BM - 1) / BM;
+  p.row_tiles = (int32_t)row_tiles;
+  p.col_tiles = (int32_t)((p.N + BN - 1) / BN);
+  p.swizzle = 4;
+  const int64_t total = row_tiles * p.col_tiles, most = (int64_t)cus * (160 * 1024 / C::LDS);
+  const uint32_t grid = (uint32_t)(total < most ? total : most);
+  p.remap = grid % 8 == 0;
+  mx4_gemm_tiled<T, BM, BN, NW, NS><<<dim3(grid), dim3(C::THREADS), C::LDS, s>>>(p);
+  return hipGetLastError() == hipSuccess ? FO_OK : FO_ERR_HIP;
+}
+
+template <typename T>
+int launch_any(const Mx4Params &p, hipStream_t s) {
+  int dev = 0, cus = 0;
+  if (hipGetDevice(&dev) != hipSuccess ||
+      hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0)
+    return FO_ERR_HIP;
+  auto tiles = [&](int64_t bm, int64_t bn) { return ((p.M + bm - 1) / bm + (p.problems - 1) / 2) * ((p.N + bn - 1) / bn); };
+  if (tiles(256, 256) >= cus) return launch_tiled<T, 256, 256, 8, 2>(p, cus, s);
+  if (tiles(128, 128) >= cus) return launch_tiled<T, 128, 128, 4, 2>(p, cus, s);
+  return launch_tiled<T, 64, 64, 4, 4>(p, cus, s);
 }
 
 }  // namespace
@@ -97,13 +395,7 @@ int launch_mx4_gemm(const void *a_codes, const void *a_scales, const void *b_cod
   p.nb = (int32_t)(K / 32);
   p.problems = problems;
   p.row_ends = row_ends;
-  const int64_t grid = ((M + 15) / 16 + (problems - 1)) * ((N + 15) / 16);
-  if (grid > 0x7FFFFFFF) return FO_ERR_UNSUPPORTED;
-  if (dtype == FO_BF16)
-    mx4_gemm_simple<__bf16><<<dim3((uint32_t)grid), 64, 0, s>>>(p);
-  else
-    mx4_gemm_simple<_Float16><<<dim3((uint32_t)grid), 64, 0, s>>>(p);
-  return hipGetLastError() == hipSuccess ? FO_OK : FO_ERR_HIP;
+  return dtype == FO_BF16 ? launch_any<__bf16>(p, s) : launch_any<_Float16>(p, s);
 }
 
 }  // namespace fo

@@ -70,7 +70,7 @@ int fo_mx4_gemm(const void *a_codes, const void *a_scales, const void *b_codes, 
                 hipStream_t stream) {
   if (M < 0 || N < 1 || K < 1 || N % 8 || K % 32 || !is_16bit(dtype)) return FO_ERR_INVALID;
   if (problems < 1 || (row_ends ? !aligned(row_ends, 4) : problems != 1)) return FO_ERR_INVALID;
-  if (problems > 4096 || M >= (1 << 30) || N >= (1 << 30) || K >= (1 << 22)) return FO_ERR_UNSUPPORTED;
+  if (problems > 4096 || M >= (1 << 30) || N >= (1 << 22) || K >= (1 << 22)) return FO_ERR_UNSUPPORTED;
   if (M == 0) return FO_OK;
   if (!aligned(a_codes, 16) || !aligned(a_scales, 16) || !aligned(b_codes, 16) || !aligned(b_scales, 16) ||
       !aligned(out, 16))

@@ -66,7 +66,7 @@ int fo_mx4_dequantize(const void *codes, const void *scales, int64_t rows, int64
  *             of A (from 0 for p = 0), which may be none.  Read on the device;
  *             values outside [0, M] are taken as the nearest bound.  Rows from
  *             row_ends[problems - 1] on are not written.
- * 1 <= problems <= 4096; M, N < 2^30.
+ * 1 <= problems <= 4096; M < 2^30; N < 2^22.
  */
 int fo_mx4_gemm(const void *a_codes, const void *a_scales, const void *b_codes, const void *b_scales, void *out,
                 int64_t M, int64_t N, int64_t K, int32_t dtype, int32_t problems, const int32_t *row_ends,

@@ -141,6 +141,25 @@ GEMM_SIZES = [(1, 8, 32), (1, 16, 256), (1, 1032, 2752), (3, 40, 96), (16, 64, 5
               (513, 776, 512), (1, 24, 16384), (40, 16, 8192)]
 
 
+# enough tiles for the larger tile shapes, with partial tiles on both edges and partial last slices
+LARGE = [(1025, 4104, 32), (1100, 4240, 800), (2050, 8200, 96), (2100, 8328, 544), (4096, 4096, 256), (2305, 8200, 1312)]
+
+
+@pytest.mark.parametrize("M, N, K", LARGE)
+def test_gemm_large_tiles(M, N, K):
+    dtype = "bf16" if K % 64 else "fp16"
+    got, _ = check_gemm(random_form(M, M, K, 119, 126), random_form(N, N, K, 119, 126), dtype, what="large")
+
+
+@pytest.mark.parametrize("ends", [[1200, 1201, 1201, 2500], [0, 700, 2500]])
+def test_gemm_large_tiles_of_stacked_problems(ends):
+    """Long stacks: the largest tiles, tiles cut at every problem's end, an empty problem, rows of no problem."""
+    N, K = 4104 if len(ends) == 4 else 8200, 288
+    a, b = random_form(3, 2600, K, 119, 126), random_form(4, N * len(ends), K, 119, 126)
+    a[1][650, 2] = b[1][N + 77, 8] = 255
+    check_gemm(a, b, "bf16", ends, what="large stacked")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("M, N, K", GEMM_SIZES)
 def test_gemm_within_its_rounding(M, N, K, dtype):

@@ -61,7 +61,7 @@ GEMM = dict(a=16, sa=16, b=16, sb=16, out=16, M=4, N=8, K=32, dtype=0, problems=
     (dict(M=-1), INVALID), (dict(N=0), INVALID), (dict(N=12), INVALID), (dict(K=0), INVALID), (dict(K=48), INVALID),
     (dict(dtype=2), INVALID), (dict(problems=0), INVALID), (dict(problems=2), INVALID), (dict(ends=6), INVALID),
     (dict(a=0), INVALID), (dict(sa=8), INVALID), (dict(b=24), INVALID), (dict(sb=0), INVALID), (dict(out=8), INVALID),
-    (dict(M=1 << 30), UNSUPPORTED), (dict(N=1 << 30), UNSUPPORTED), (dict(K=1 << 22), UNSUPPORTED),
+    (dict(M=1 << 30), UNSUPPORTED), (dict(N=1 << 22), UNSUPPORTED), (dict(K=1 << 22), UNSUPPORTED),
     (dict(problems=4097, ends=16), UNSUPPORTED), (dict(M=0, a=0, out=0), 0),
 ])
 def test_gemm(change, code):
