@@ -422,7 +422,7 @@ int launch_typed(const MoeParams &p, hipStream_t s) {
 
 int launch_moe(const fo_moe_desc &d, int32_t tokens, const void *x, const void *router, const void *gate_up,
                const void *gate_up_scales, const void *down, const void *down_scales, void *out, int32_t *ids,
-               float *weights, void *workspace, hipStream_t s) {
+               float *weights, void *workspace, int cus, hipStream_t s) {
   const MoeLayout l = moe_layout(d);
   char *ws = static_cast<char *>(workspace);
   MoeParams p{};

@@ -368,11 +368,7 @@ int launch_tiled(Mx4Params p, int cus, hipStream_t s) {
 }
 
 template <typename T>
-int launch_any(const Mx4Params &p, hipStream_t s) {
-  int dev = 0, cus = 0;
-  if (hipGetDevice(&dev) != hipSuccess ||
-      hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0)
-    return FO_ERR_HIP;
+int launch_any(const Mx4Params &p, int cus, hipStream_t s) {
   auto tiles = [&](int64_t bm, int64_t bn) { return ((p.M + bm - 1) / bm + (p.problems - 1) / 2) * ((p.N + bn - 1) / bn); };
   if (tiles(256, 256) >= cus) return launch_tiled<T, 256, 256, 8, 2>(p, cus, s);
   if (tiles(128, 128) >= cus) return launch_tiled<T, 128, 128, 4, 2>(p, cus, s);
@@ -383,7 +379,7 @@ int launch_any(const Mx4Params &p, hipStream_t s) {
 
 int launch_mx4_gemm(const void *a_codes, const void *a_scales, const void *b_codes, const void *b_scales, void *out,
                     int64_t M, int64_t N, int64_t K, int32_t dtype, int32_t problems, const int32_t *row_ends,
-                    hipStream_t s) {
+                    int cus, hipStream_t s) {
   Mx4Params p{};
   p.a = static_cast<const uint8_t *>(a_codes);
   p.as = static_cast<const uint8_t *>(a_scales);
@@ -395,7 +391,7 @@ int launch_mx4_gemm(const void *a_codes, const void *a_scales, const void *b_cod
   p.nb = (int32_t)(K / 32);
   p.problems = problems;
   p.row_ends = row_ends;
-  return dtype == FO_BF16 ? launch_any<__bf16>(p, s) : launch_any<_Float16>(p, s);
+  return dtype == FO_BF16 ? launch_any<__bf16>(p, cus, s) : launch_any<_Float16>(p, cus, s);
 }
 
 }  // namespace fo

@@ -60,7 +60,7 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t *cod
 }  // namespace
 
 int launch_mx4_quantize(const void *x, int64_t rows, int64_t cols, int64_t ld, int32_t dtype, void *codes,
-                        void *scales, hipStream_t s) {
+                        void *scales, int cus, hipStream_t s) {
   const int64_t n = rows * (((cols + 31) / 32 + 7) / 8 * 8), grid = (n + kThreads - 1) / kThreads;
   if (grid > 0x7FFFFFFF) return FO_ERR_UNSUPPORTED;
   auto *c = static_cast<uint8_t *>(codes), *sc = static_cast<uint8_t *>(scales);
@@ -72,7 +72,7 @@ int launch_mx4_quantize(const void *x, int64_t rows, int64_t cols, int64_t ld, i
 }
 
 int launch_mx4_dequantize(const void *codes, const void *scales, int64_t rows, int64_t cols, int32_t out_type,
-                          void *out, hipStream_t s) {
+                          void *out, int cus, hipStream_t s) {
   const int64_t n = rows * ((cols + 31) / 32), grid = (n + kThreads - 1) / kThreads;
   if (grid > 0x7FFFFFFF) return FO_ERR_UNSUPPORTED;
   auto *c = static_cast<const uint8_t *>(codes), *sc = static_cast<const uint8_t *>(scales);

@@ -11,21 +11,22 @@ bool aligned(const void *ptr, uintptr_t to) { return ptr && (reinterpret_cast<ui
 
 bool is_16bit(int32_t dtype) { return dtype == FO_BF16 || dtype == FO_FP16; }
 
-// FO_OK if the current device runs the kernels.  The answer of each device is
-// kept: asking the runtime for a device's name takes longer than a small call.
-int device_status() {
+// CUs of the current device, or a status: FO_ERR_UNSUPPORTED for one that does
+// not run the kernels.  The answer of each device is kept: asking the runtime
+// for it takes longer than a small call.
+int device_cus() {
   constexpr int kDevices = 64;
-  static std::atomic<int8_t> known[kDevices];  // 0: not asked yet, 1: gfx950, -1: another
+  static std::atomic<int32_t> known[kDevices];  // 0: not asked yet; CUs; < 0: a status
   int dev = -1;
   if (hipGetDevice(&dev) != hipSuccess) return FO_ERR_HIP;
-  int8_t k = dev >= 0 && dev < kDevices ? known[dev].load(std::memory_order_relaxed) : 0;
+  int32_t k = dev >= 0 && dev < kDevices ? known[dev].load(std::memory_order_relaxed) : 0;
   if (k == 0) {
     hipDeviceProp_t prop;
-    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return FO_ERR_HIP;
-    k = fo_arch_supported(prop.gcnArchName) ? 1 : -1;
+    if (hipGetDeviceProperties(&prop, dev) != hipSuccess || prop.multiProcessorCount <= 0) return FO_ERR_HIP;
+    k = fo_arch_supported(prop.gcnArchName) ? prop.multiProcessorCount : FO_ERR_UNSUPPORTED;
     if (dev >= 0 && dev < kDevices) known[dev].store(k, std::memory_order_relaxed);
   }
-  return k > 0 ? FO_OK : FO_ERR_UNSUPPORTED;
+  return k;
 }
 
 int moe_desc_status(const fo_moe_desc *d) {
@@ -51,8 +52,9 @@ int fo_mx4_quantize(const void *x, int64_t rows, int64_t cols, int64_t ld, int32
   if (rows == 0) return FO_OK;
   if (!aligned(x, 2) || !aligned(codes, 16) || !aligned(scales, 16)) return FO_ERR_INVALID;
   if (rows > (1ll << 40) || ld > (1ll << 40) / rows) return FO_ERR_UNSUPPORTED;
-  if (const int rc = device_status()) return rc;
-  return fo::launch_mx4_quantize(x, rows, cols, ld, dtype, codes, scales, stream);
+  const int cus = device_cus();
+  if (cus < 0) return cus;
+  return fo::launch_mx4_quantize(x, rows, cols, ld, dtype, codes, scales, cus, stream);
 }
 
 int fo_mx4_dequantize(const void *codes, const void *scales, int64_t rows, int64_t cols, int32_t out_type, void *out,
@@ -61,8 +63,9 @@ int fo_mx4_dequantize(const void *codes, const void *scales, int64_t rows, int64
   if (rows == 0) return FO_OK;
   if (!aligned(codes, 16) || !aligned(scales, 16) || !aligned(out, out_type == FO_FP32 ? 4 : 2)) return FO_ERR_INVALID;
   if (rows > (1ll << 40) || cols > (1ll << 40) / rows) return FO_ERR_UNSUPPORTED;
-  if (const int rc = device_status()) return rc;
-  return fo::launch_mx4_dequantize(codes, scales, rows, cols, out_type, out, stream);
+  const int cus = device_cus();
+  if (cus < 0) return cus;
+  return fo::launch_mx4_dequantize(codes, scales, rows, cols, out_type, out, cus, stream);
 }
 
 int fo_mx4_gemm(const void *a_codes, const void *a_scales, const void *b_codes, const void *b_scales, void *out,
@@ -75,8 +78,10 @@ int fo_mx4_gemm(const void *a_codes, const void *a_scales, const void *b_codes, 
   if (!aligned(a_codes, 16) || !aligned(a_scales, 16) || !aligned(b_codes, 16) || !aligned(b_scales, 16) ||
       !aligned(out, 16))
     return FO_ERR_INVALID;
-  if (const int rc = device_status()) return rc;
-  return fo::launch_mx4_gemm(a_codes, a_scales, b_codes, b_scales, out, M, N, K, dtype, problems, row_ends, stream);
+  const int cus = device_cus();
+  if (cus < 0) return cus;
+  return fo::launch_mx4_gemm(a_codes, a_scales, b_codes, b_scales, out, M, N, K, dtype, problems, row_ends,
+                             cus, stream);
 }
 
 int fo_moe_workspace_bytes(const fo_moe_desc *desc, int64_t *bytes) {
@@ -100,9 +105,10 @@ int fo_moe_forward(const fo_moe_desc *desc, int64_t tokens, const void *x, const
                                   : gate_up_scales || down_scales)
     return FO_ERR_INVALID;
   if ((ids && !aligned(ids, 4)) || (weights && !aligned(weights, 4))) return FO_ERR_INVALID;
-  if (const int rc = device_status()) return rc;
+  const int cus = device_cus();
+  if (cus < 0) return cus;
   return fo::launch_moe(*desc, (int32_t)tokens, x, router, gate_up, gate_up_scales, down, down_scales, out, ids,
-                        weights, workspace, stream);
+                        weights, workspace, cus, stream);
 }
 
 }  // extern "C"

@@ -10,12 +10,12 @@
 namespace fo {
 
 int launch_mx4_quantize(const void *x, int64_t rows, int64_t cols, int64_t ld, int32_t dtype, void *codes,
-                        void *scales, hipStream_t s);
+                        void *scales, int cus, hipStream_t s);
 int launch_mx4_dequantize(const void *codes, const void *scales, int64_t rows, int64_t cols, int32_t out_type,
-                          void *out, hipStream_t s);
+                          void *out, int cus, hipStream_t s);
 int launch_mx4_gemm(const void *a_codes, const void *a_scales, const void *b_codes, const void *b_scales, void *out,
                     int64_t M, int64_t N, int64_t K, int32_t dtype, int32_t problems, const int32_t *row_ends,
-                    hipStream_t s);
+                    int cus, hipStream_t s);
 
 // Parts of a layer's workspace, as byte offsets; each begins on 256 bytes.
 struct MoeLayout {
@@ -50,6 +50,6 @@ inline MoeLayout moe_layout(const fo_moe_desc &d) {
 }
 int launch_moe(const fo_moe_desc &d, int32_t tokens, const void *x, const void *router, const void *gate_up,
                const void *gate_up_scales, const void *down, const void *down_scales, void *out, int32_t *ids,
-               float *weights, void *workspace, hipStream_t s);
+               float *weights, void *workspace, int cus, hipStream_t s);
 
 }  // namespace fo

@@ -10,8 +10,8 @@ from __future__ import annotations
 import ctypes as C
 from typing import Optional
 
-from . import _DTYPES, _check, _stream
-from .mx4 import _current, _new, _on, _ops, mx4_shapes
+from . import _DTYPES
+from .mx4 import _buffer, _device, _done, _new, _on_stream, _ops, mx4_shapes
 
 __all__ = ["Moe"]
 
@@ -24,16 +24,11 @@ class _MoeDesc(C.Structure):
                 ("renormalize", C.c_int32), ("max_tokens", C.c_int32)]
 
 
-def _buffer(x, name: str, numel: int, itemsize: int, device) -> int:
+def _sized(x, name: str, numel: int, itemsize: int, device: int) -> int:
     """Address of a contiguous device tensor of this many elements (of any shape) of this size."""
     if x.numel() != numel:
         raise ValueError(f"{name}: {x.numel()} elements, expected {numel}")
-    if x.element_size() != itemsize:
-        raise ValueError(f"{name}: element size {x.element_size()} != {itemsize}")
-    if not x.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    _on(x, name, device)
-    return x.data_ptr()
+    return _buffer(x, name, itemsize, device)
 
 
 class Moe:
@@ -61,49 +56,54 @@ class Moe:
         self._d = _MoeDesc(self.hidden, self.ffn, self.experts, self.top_k, self.first_expert, self.local_experts,
                            _DTYPES[dtype], _WEIGHTS[weights], int(self.renormalize), self.max_tokens)
         n = C.c_int64()
-        lib = _ops()
-        _check(lib.fo_moe_workspace_bytes(C.byref(self._d), C.byref(n)), "fo_moe_workspace_bytes")
-        self.workspace_bytes = n.value
         self._ref = C.byref(self._d)
+        _done(_ops().fo_moe_workspace_bytes(self._ref, C.byref(n)), "fo_moe_workspace_bytes")
+        self.workspace_bytes = n.value
+        # elements of each matrix: itself, or its codes and its scales
+        rows = (self.local_experts * 2 * self.ffn, self.hidden), (self.local_experts * self.hidden, self.ffn)
+        if weights == "16":
+            self._numel = [(r * c,) for r, c in rows]
+        else:
+            self._numel = [(c[0] * c[1], s[0] * s[1] * s[2]) for c, s in (mx4_shapes(*rc) for rc in rows)]
 
     def new_workspace(self, device="cuda"):
         """A zeroed workspace, uint8 [workspace_bytes]."""
         import torch
         return torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=device)
 
-    def _matrix(self, m, name: str, rows: int, cols: int, device):
-        """(address, address of the scales or 0) of one of the experts' matrices, its rows stacked."""
-        if self.weights == "16":
-            return _buffer(m, name, rows * cols, 2, device), 0
+    def _matrix(self, m, name: str, numel, device: int):
+        """(address, address of the scales or None) of one of the experts' matrices."""
+        if len(numel) == 1:
+            return _sized(m, name, numel[0], 2, device), None
         codes, scales = m
-        c, s = mx4_shapes(rows, cols)
-        return (_buffer(codes, name + " codes", c[0] * c[1], 1, device),
-                _buffer(scales, name + " scales", s[0] * s[1] * s[2], 1, device))
+        return _sized(codes, name, numel[0], 1, device), _sized(scales, name, numel[1], 1, device)
 
     def forward(self, x, router, gate_up, down, workspace, out=None, picks=None, stream=None):
         """out [tokens, hidden] of x [tokens, hidden] (``fo_moe_forward``).
 
         ``picks``: optional (ids int32, weights float32), each [tokens, top_k],
         that receive the picked experts and their weights."""
-        import torch
+        o = _ops()
+        wanted = o.types[self.dtype]
         if x.dim() != 2 or x.shape[1] != self.hidden:
             raise ValueError(f"x: shape {tuple(x.shape)}, expected [tokens, {self.hidden}]")
-        device, tokens = _current(x, "x"), x.shape[0]
+        if x.dtype not in (wanted, o.torch.int16):
+            raise ValueError(f"x: {x.dtype}, the layer computes in {self.dtype}")
+        device, tokens = _device(x, "x"), x.shape[0]
         if tokens > self.max_tokens:
             raise ValueError(f"x: {tokens} tokens, the layer is for at most {self.max_tokens}")
-        wanted = torch.bfloat16 if self.dtype == "bf16" else torch.float16
-        if x.dtype not in (wanted, torch.int16):
-            raise ValueError(f"x: {x.dtype}, the layer computes in {self.dtype}")
         if out is None:
-            out, = _new(stream, device, ((tokens, self.hidden), wanted))
-        n, L, D, F = tokens * self.top_k, self.local_experts, self.hidden, self.ffn
-        gu, gus = self._matrix(gate_up, "gate_up", L * 2 * F, D, device)
-        dn, dns = self._matrix(down, "down", L * D, F, device)
-        ids, wts = (0, 0) if picks is None else (_buffer(picks[0], "picked ids", n, 4, device),
-                                                 _buffer(picks[1], "picked weights", n, 4, device))
-        _check(_ops().fo_moe_forward(
-            self._ref, tokens, _buffer(x, "x", tokens * D, 2, device),
-            _buffer(router, "router", self.experts * D, 2, device), gu, gus, dn, dns,
-            _buffer(out, "out", tokens * D, 2, device), ids, wts,
-            _buffer(workspace, "workspace", self.workspace_bytes, 1, device), _stream(stream)), "fo_moe_forward")
+            out = _new(x, (tokens, self.hidden), wanted, stream)
+        gu, gus = self._matrix(gate_up, "gate_up", self._numel[0], device)
+        dn, dns = self._matrix(down, "down", self._numel[1], device)
+        ids = wts = None
+        if picks is not None:
+            ids = _sized(picks[0], "picked ids", tokens * self.top_k, 4, device)
+            wts = _sized(picks[1], "picked weights", tokens * self.top_k, 4, device)
+        n = tokens * self.hidden
+        _done(o.fo_moe_forward(
+            self._ref, tokens, _buffer(x, "x", 2, device), _sized(router, "router", self.experts * self.hidden, 2, device),
+            gu, gus, dn, dns, _sized(out, "out", n, 2, device), ids, wts,
+            _sized(workspace, "workspace", self.workspace_bytes, 1, device), _on_stream(stream, device)),
+            "fo_moe_forward")
         return out
