@@ -1,20 +1,32 @@
 // Mixture-of-experts layer for a few tokens: three kernels.
-//   router  logits of every expert, then (last workgroup to finish) the picks,
-//           their weights, and each active expert's token mask;
+//   router  logits of every expert, the picks and their weights, and the active
+//           experts' list;
 //   up      h = silu(gate . x) * (up . x) for every (active expert, picked token);
 //   down    out = sum over active experts of w * (down . h).
-// The work is reading each active expert's weights once.  The weights' rows are
-// one operand of the matrix instructions (16 rows per wave), the tokens the
-// other (columns, 16 per tile), so a weight is read once for all its tokens.
+// The work is reading each active expert's weights once; nothing else is large.
+// The weights' rows are one operand of the matrix instructions (16 rows a
+// block), the tokens the other (columns, 16 a tile), so a weight is read once
+// for all its tokens.  Weights go from memory straight to registers, each wave
+// a contiguous share of K with the next group's loads in flight while a group
+// is multiplied; nothing is shared between waves but the final sums.
 #include <type_traits>
 
 #include "../ops_internal.h"
+#include "buffer.h"
 #include "mx4.h"
 
 namespace fo {
 namespace {
 
-constexpr int kMaxTokens = 64, kMaxTiles = kMaxTokens / 16, kMaxTopK = 16, kMaxExperts = 1024;
+constexpr int kMaxTokens = 64, kMaxTopK = 16, kMaxExperts = 1024;
+constexpr uint32_t kOutOfRange = 0xC0000000u;  // a byte offset past every buffer resource made here
+
+// One active expert: its tokens, and the first of their rows of h (ascending tokens).
+struct MoeSlot {
+  int32_t expert;  // local index; -1: no expert
+  int32_t row;
+  uint64_t mask;
+};
 
 struct MoeParams {
   const uint16_t *x, *router;
@@ -22,15 +34,17 @@ struct MoeParams {
   uint16_t *out;
   int32_t *ids_out;
   float *wts_out;
-  uint32_t *counter;
-  int32_t *head;
-  uint64_t *masks;
+  uint32_t *counters;  // [0]: token tiles done; [1 + tile]: router workgroups done; then down's tiles; all zero between calls
+  int32_t *head;       // number of active experts
+  MoeSlot *slots;
+  float *row_w;        // weight of each row of h
   int32_t *ids;
   float *wts;
   float *logits;
-  uint16_t *x_split;  // [2][tokens][D]
-  uint16_t *h;        // [2][tokens * top_k][F]
-  int32_t T, D, F, E, top_k, first, local, renorm, router_wgs;
+  uint16_t *x_split;   // [2][tokens][D]
+  uint16_t *h;         // [2][rows][F]
+  float *partial;      // [splits][T][D]
+  int32_t T, D, F, E, top_k, first, local, renorm, expert_wgs, tiles, most, splits;
 };
 
 template <typename T>
@@ -56,92 +70,137 @@ __device__ __forceinline__ u32x4 mx4_to_bf16(uint32_t codes, float scale) {
   return v;
 }
 
-__device__ __forceinline__ u32x4 load16(const void *p) { return *reinterpret_cast<const u32x4 *>(p); }
-
-// Order of the logits as unsigned integers: a NaN above every number, -0 as +0.
+// Order of the logits as unsigned integers: a NaN above every number, -0 as +0; 0 is below all.
 __device__ __forceinline__ uint32_t order_key(float l) {
   if (l != l) return 0xFFFFFFFFu;
   const uint32_t b = __float_as_uint(l + 0.0f);
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 32; d > 0; d /= 2) v += __shfl_xor(v, d);
-  return v;
+// Reductions over the 64 lanes by data-parallel moves (row shifts, then row
+// broadcasts: lane 63 ends up with the whole), a few cycles a step where a
+// shuffle through LDS takes tens.
+template <int CTRL>
+__device__ __forceinline__ uint32_t moved(uint32_t v, uint32_t none) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, CTRL, 0xF, 0xF, false);
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = max(v, moved<0x111>(v, 0));
+  v = max(v, moved<0x112>(v, 0));
+  v = max(v, moved<0x114>(v, 0));
+  v = max(v, moved<0x118>(v, 0));
+  v = max(v, moved<0x142>(v, 0));
+  v = max(v, moved<0x143>(v, 0));
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+__device__ __forceinline__ float wave_sum(float f) {
+  auto add = [](float a, uint32_t b) { return a + __uint_as_float(b); };
+  f = add(f, moved<0x111>(__float_as_uint(f), 0));
+  f = add(f, moved<0x112>(__float_as_uint(f), 0));
+  f = add(f, moved<0x114>(__float_as_uint(f), 0));
+  f = add(f, moved<0x118>(__float_as_uint(f), 0));
+  // rows of 16 hold their sums in their last lanes; the broadcasts reach whole rows, of which the last lane is used
+  f = add(f, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(f), 0x142, 0xA, 0xF, false));
+  f = add(f, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(f), 0x143, 0xC, 0xF, false));
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(f), 63));
 }
 
-// Picks of token t by one wave: expert e of lane e % 64.
-__device__ __forceinline__ void select_token(const MoeParams &p, int t, int lane, uint64_t *mask) {
-  constexpr int R = kMaxExperts / 64;
+// Values that another workgroup of the same launch reads: written through to,
+// and read from, the device's point of coherence.
+__device__ __forceinline__ void put(float *p, float v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void put(int32_t *p, int32_t v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename V>
+__device__ __forceinline__ V get(const V *p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// The workgroup's put()s are complete, then it is counted; true in the one of
+// `of` workgroups that is counted last, which also clears the counter.
+__device__ __forceinline__ bool arrive_last(uint32_t *counter, uint32_t of) {
+  __shared__ uint32_t ticket;
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): every store of this wave has reached the point of coherence
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    ticket = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (ticket == of - 1) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  const bool last = ticket == of - 1;
+  __syncthreads();  // the next use may overwrite the ticket
+  return last;
+}
+
+// Picks of one token by one wave; expert e is in lane e % 64, register e / 64.
+// Lane j < top_k returns pick j and its weight.
+template <int R, typename Load>
+__device__ __forceinline__ void select_token(const MoeParams &p, int lane, Load &&logit, int *id, float *weight) {
   float l[R];
   uint32_t key[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int e = i * 64 + lane;
-    l[i] = e < p.E ? p.logits[(int64_t)t * p.E + e] : 0.0f;
-    key[i] = e < p.E ? order_key(l[i]) : 0u;  // 0 is below the key of every logit
+    l[i] = e < p.E ? logit(e) : 0.0f;
+    key[i] = e < p.E ? order_key(l[i]) : 0u;
   }
-  float top = 0, sum = 0, picked = 0, my_w = 0;
-  int my_id = 0;
+  float top = 0, sum = 0, picked = 0, w = 0;
+  int mine = 0;
   for (int j = 0; j < p.top_k; ++j) {
-    uint64_t best = 0;
+    uint32_t best = 0;
 #pragma unroll
-    for (int i = 0; i < R; ++i)
-      if (i * 64 < p.E) {
-        const uint64_t k = ((uint64_t)key[i] << 32) | (uint32_t)~(i * 64 + lane);
-        best = k > best ? k : best;
-      }
-#pragma unroll
-    for (int d = 32; d > 0; d /= 2) {
-      const uint64_t o = __shfl_xor((unsigned long long)best, d);
-      best = o > best ? o : best;
-    }
-    const int e = (int)~(uint32_t)best;
+    for (int i = 0; i < R; ++i) best = max(best, key[i]);
+    best = wave_max(best);
+    int at = -1;  // lowest index that holds it
     float le = 0;
 #pragma unroll
-    for (int i = 0; i < R; ++i)
-      if (e == i * 64 + lane) {
-        le = l[i];
-        key[i] = 0;
+    for (int i = 0; i < R; ++i) {
+      const uint64_t has = __ballot(key[i] == best);
+      if (at < 0 && has) {
+        const int src = __builtin_ctzll(has);
+        at = i * 64 + src;
+        le = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(l[i]), src));
+        if (lane == src) key[i] = 0;
       }
-    le = __shfl(le, e & 63);
+    }
     if (j == 0) {
       top = le;
 #pragma unroll
-      for (int i = 0; i < R; ++i)
-        if (i * 64 + lane < p.E) sum += __expf(l[i] - top);
+      for (int i = 0; i < R; ++i) sum += i * 64 + lane < p.E ? __expf(l[i] - top) : 0.0f;
       sum = wave_sum(sum);
     }
-    const float w = __expf(le - top);
-    picked += w;
+    const float v = __expf(le - top);
+    picked += v;
     if (lane == j) {
-      my_id = e;
-      my_w = w;
+      mine = at;
+      w = v;
     }
-    const int here = e - p.first;
-    if (lane == 0 && here >= 0 && here < p.local) atomicOr((unsigned long long *)&mask[here], 1ull << t);
   }
-  if (lane < p.top_k) {
-    const float w = my_w / (p.renorm ? picked : sum);
-    p.ids[t * p.top_k + lane] = my_id;
-    p.wts[t * p.top_k + lane] = w;
-    if (p.ids_out) p.ids_out[t * p.top_k + lane] = my_id;
-    if (p.wts_out) p.wts_out[t * p.top_k + lane] = w;
-  }
+  *id = mine;
+  *weight = w / (p.renorm ? picked : sum);
 }
 
-// Router: 16 experts per workgroup, its waves each a share of the hidden size.
-constexpr int kRouterWaves = 8;
+// Router.  A workgroup multiplies 16 experts with 16 tokens, its 16 waves each a
+// share of the hidden size.  The last workgroup of a token tile picks for its
+// tokens, a wave each; the last tile lists the active experts.
+constexpr int kRouterWaves = 16;
 template <typename T>
 __global__ __launch_bounds__(64 * kRouterWaves) void moe_router(MoeParams p) {
-  __shared__ float red[kRouterWaves][kMaxTiles][64][4];
+  __shared__ float red[kRouterWaves][64][4];
+  __shared__ float tile_logits[16][16];
+  __shared__ int32_t sel_id[kMaxTokens * kMaxTopK];
+  __shared__ float sel_w[kMaxTokens * kMaxTopK];
   __shared__ uint64_t mask[kMaxExperts];
-  __shared__ uint32_t ticket;
+  __shared__ int32_t row_of[kMaxExperts];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
-  if ((int)blockIdx.x >= p.router_wgs) {  // the workgroups that split fp16 tokens into two bf16 values
-    const int64_t n = (int64_t)p.T * p.D, step = (int64_t)(gridDim.x - p.router_wgs) * blockDim.x;
-    for (int64_t i = (int64_t)(blockIdx.x - p.router_wgs) * blockDim.x + tid; i < n; i += step) {
+  constexpr int kThreads = 64 * kRouterWaves;
+  const int wgs = p.expert_wgs * p.tiles;
+  if ((int)blockIdx.x >= wgs) {  // the workgroups that split fp16 tokens into two bf16 values
+    const int64_t n = (int64_t)p.T * p.D, step = (int64_t)(gridDim.x - wgs) * kThreads;
+    for (int64_t i = (int64_t)(blockIdx.x - wgs) * kThreads + tid; i < n; i += step) {
       const float v = (float)reinterpret_cast<const T *>(p.x)[i];
       const __bf16 hi = (__bf16)v;
       // an infinity or a NaN goes whole into the first part
@@ -151,271 +210,461 @@ __global__ __launch_bounds__(64 * kRouterWaves) void moe_router(MoeParams p) {
     }
     return;
   }
-  const int e = blockIdx.x * 16 + r, tiles = (p.T + 15) / 16;
-  f32x4 acc[kMaxTiles] = {};
-  for (int k0 = wave * 32; k0 < p.D; k0 += kRouterWaves * 32) {
-    const int k = k0 + g * 8;
-    u32x4 a = {};
-    if (e < p.E && k < p.D) a = load16(p.router + (int64_t)e * p.D + k);
+  const int tile = blockIdx.x / p.expert_wgs, e0 = (blockIdx.x % p.expert_wgs) * 16, t0 = tile * 16;
+  const int rows_e = min(16, p.E - e0), rows_t = min(16, p.T - t0);
+  {
+    const uint32_t pitch = (uint32_t)p.D * 2u;
+    const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.router + (int64_t)e0 * p.D, rows_e * pitch);
+    const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.x + (int64_t)t0 * p.D, rows_t * pitch);
+    f32x4 acc = {};
+    constexpr int U = 8;
+    const int steps = (p.D + 31) / 32;
+    for (int s = wave; s < steps; s += kRouterWaves * U) {
+      u32x4 a[U], b[U];
 #pragma unroll
-    for (int c = 0; c < kMaxTiles; ++c)
-      if (c < tiles) {
-        u32x4 b = {};
-        if (c * 16 + r < p.T && k < p.D) b = load16(p.x + (int64_t)(c * 16 + r) * p.D + k);
-        acc[c] = mma16<T>(a, b, acc[c]);
+      for (int u = 0; u < U; ++u) {
+        const int k = (s + u * kRouterWaves) * 32 + g * 8;
+        const uint32_t at = k < p.D ? r * pitch + k * 2u : kOutOfRange;
+        a[u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ra, at, 0, 0));
+        b[u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rb, at, 0, 0));
       }
-  }
 #pragma unroll
-  for (int c = 0; c < kMaxTiles; ++c) *reinterpret_cast<f32x4 *>(red[wave][c][lane]) = acc[c];
-  __syncthreads();
-  for (int i = tid; i < tiles * 256; i += 64 * kRouterWaves) {
-    const int c = i >> 8, l = (i >> 2) & 63, q = i & 3;
-    float s = 0;
-    for (int w = 0; w < kRouterWaves; ++w) s += red[w][c][l][q];
-    const int t = c * 16 + (l & 15), ee = blockIdx.x * 16 + (l >> 4) * 4 + q;
-    if (t < p.T && ee < p.E) p.logits[(int64_t)t * p.E + ee] = s;
+      for (int u = 0; u < U; ++u) acc = mma16<T>(a[u], b[u], acc);
+    }
+    *reinterpret_cast<f32x4 *>(red[wave][lane]) = acc;
   }
-  // the last workgroup to arrive sees every logit and picks
-  __threadfence();
+  for (int i = tid; i < p.local; i += kThreads) mask[i] = 0;
   __syncthreads();
-  if (tid == 0)
-    ticket = __hip_atomic_fetch_add(p.counter, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-  for (int i = tid; i < p.local; i += 64 * kRouterWaves) mask[i] = 0;
+  if (tid < 256) {
+    const int l = tid >> 2, q = tid & 3, t = l & 15, e = (l >> 4) * 4 + q;
+    float s = 0;
+#pragma unroll
+    for (int w = 0; w < kRouterWaves; ++w) s += red[w][l][q];
+    tile_logits[t][e] = s;
+    if (p.expert_wgs > 1 && t < rows_t && e < rows_e) put(&p.logits[(int64_t)(t0 + t) * p.E + e0 + e], s);
+  }
+  if (p.expert_wgs > 1) {
+    if (!arrive_last(&p.counters[1 + tile], p.expert_wgs)) return;
+  } else {
+    __syncthreads();
+  }
+  if (wave < rows_t) {
+    const int t = t0 + wave;
+    int id = 0;
+    float w = 0;
+    auto far = [&](int e) { return get(&p.logits[(int64_t)t * p.E + e]); };
+    if (p.expert_wgs == 1)
+      select_token<1>(p, lane, [&](int e) { return tile_logits[wave][e]; }, &id, &w);
+    else if (p.E <= 64)
+      select_token<1>(p, lane, far, &id, &w);
+    else if (p.E <= 256)
+      select_token<4>(p, lane, far, &id, &w);
+    else
+      select_token<16>(p, lane, far, &id, &w);
+    if (lane < p.top_k) {
+      const int at = t * p.top_k + lane;
+      sel_id[at] = id;
+      sel_w[at] = w;
+      if (p.tiles > 1) {
+        put(&p.ids[at], id);
+        put(&p.wts[at], w);
+      }
+      if (p.ids_out) p.ids_out[at] = id;
+      if (p.wts_out) p.wts_out[at] = w;
+    }
+  }
+  const int picks = p.T * p.top_k;
+  if (p.tiles > 1) {
+    if (!arrive_last(&p.counters[0], p.tiles)) return;
+    for (int i = tid; i < picks; i += kThreads) {
+      sel_id[i] = get(&p.ids[i]);
+      sel_w[i] = get(&p.wts[i]);
+    }
+  }
   __syncthreads();
-  if (ticket != (uint32_t)p.router_wgs - 1) return;
-  __threadfence();
-  for (int t = wave; t < p.T; t += kRouterWaves) select_token(p, t, lane, mask);
+  for (int i = tid; i < picks; i += kThreads) {
+    const int e = sel_id[i] - p.first;
+    if (e >= 0 && e < p.local) atomicOr((unsigned long long *)&mask[e], 1ull << (i / p.top_k));
+  }
   __syncthreads();
   if (wave == 0) {
-    int n = 0;
-    for (int e0 = 0; e0 < p.local; e0 += 64) {
-      const uint64_t m = e0 + lane < p.local ? mask[e0 + lane] : 0;
+    int n = 0, row = 0;
+    for (int b = 0; b < p.local; b += 64) {
+      const uint64_t m = b + lane < p.local ? mask[b + lane] : 0;
       const uint64_t any = __ballot(m != 0);
+      if (!any) continue;
+      const int count = __popcll(m);
+      int before = count;  // rows of the lanes up to this one
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) {
+        const int other = __shfl_up(before, d);
+        if (lane >= d) before += other;
+      }
       if (m) {
-        const int at = n + __popcll(any & ((1ull << lane) - 1));
-        p.head[1 + at] = e0 + lane;
-        p.masks[at] = m;
+        p.slots[n + __popcll(any & ((1ull << lane) - 1))] = MoeSlot{b + lane, row + before - count, m};
+        row_of[b + lane] = row + before - count;
       }
       n += __popcll(any);
+      row += __shfl(before, 63);
     }
-    if (lane == 0) {
-      p.head[0] = n;
-      __hip_atomic_store(p.counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
+    for (int i = n + lane; i < p.most; i += 64) p.slots[i] = MoeSlot{-1, 0, 0};
+    if (lane == 0) p.head[0] = n;
+  }
+  __syncthreads();
+  for (int i = tid; i < picks; i += kThreads) {
+    const int e = sel_id[i] - p.first, t = i / p.top_k;
+    if (e >= 0 && e < p.local) p.row_w[row_of[e] + __popcll(mask[e] & ((1ull << t) - 1))] = sel_w[i];
   }
 }
 
-// Up: 16 values of h per workgroup and active expert, its waves each a share of the hidden size.
+// Weights of PARTS matrices (RB blocks of 16 rows each) times CT tiles of
+// columns that come in PL parts (1, or 2 whose sum is meant), over k in
+// [k0, k1): k0 a multiple of 32 (256 with 4-bit weights), K the row length.
+// col[c]: byte offset of this lane's column in every part; out of range: none.
+template <typename C, int PARTS, int RB, int CT, int PL>
+struct Stream16 {
+  static constexpr int NA = PARTS * RB, U = NA >= 8 ? 1 : 8 / NA;
+  __amdgpu_buffer_rsrc_t rw[PARTS], rc[PL];
+  uint32_t pitch;
+  u32x4 a[U][NA];
+  __device__ __forceinline__ void load_a(int k, int end, int r, int g) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int kk = k + u * 32 + g * 8;
+#pragma unroll
+      for (int i = 0; i < NA; ++i) {
+        const uint32_t at = kk < end ? (uint32_t)((i % RB) * 16 + r) * pitch + kk * 2u : kOutOfRange;
+        a[u][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw[i / RB], at, 0, 0));
+      }
+    }
+  }
+  __device__ __forceinline__ void run(int k0, int k1, int K, const uint32_t (&col)[CT], f32x4 (&acc)[NA][CT]) {
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, end = min(k1, K);
+    if (k0 >= end) return;
+    load_a(k0, end, r, g);
+    for (int k = k0; k < end; k += U * 32) {
+      u32x4 b[U][CT][PL], w[U][NA];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int kk = k + u * 32 + g * 8;
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          const uint32_t at = kk < end && col[c] < kOutOfRange ? col[c] + kk * 2u : kOutOfRange;
+#pragma unroll
+          for (int q = 0; q < PL; ++q)
+            b[u][c][q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rc[q], at, 0, 0));
+        }
+#pragma unroll
+        for (int i = 0; i < NA; ++i) w[u][i] = a[u][i];
+      }
+      load_a(k + U * 32, end, r, g);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+          for (int q = 0; q < PL; ++q)
+#pragma unroll
+            for (int i = 0; i < NA; ++i) acc[i][c] = mma16<C>(w[u][i], b[u][c][q], acc[i][c]);
+    }
+  }
+};
+
+// The same with 4-bit weights.  A step is a panel of 8 blocks: lane group g takes
+// blocks 2 g and 2 g + 1 of it, so that its codes are 32 and its scales 2
+// neighbouring bytes (the order of k is free as long as the columns follow it).
+template <int PARTS, int RB, int CT, int PL>
+struct Stream4 {
+  static constexpr int NA = PARTS * RB;
+  __amdgpu_buffer_rsrc_t rw[PARTS], rc[PL];
+  const uint8_t *scales[PARTS];  // of the part's first row, panel 0
+  int64_t panel;                 // bytes of a panel
+  uint32_t rows[PARTS];          // rows of the part from its first one on
+  uint32_t pitch;
+  u32x4 a[NA][2];
+  uint32_t s[NA];
+  __device__ __forceinline__ void load_a(int k, int end, int r, int g) {
+    const int b = k / 32 + g * 2, nb = end / 32;
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+      const __amdgpu_buffer_rsrc_t rs = make_rsrc(scales[i / RB] + (k / 256) * panel, rows[i / RB] * 8);
+      const uint32_t row = (uint32_t)((i % RB) * 16 + r);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        a[i][h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                rw[i / RB], b + h < nb ? row * pitch + (b + h) * 16u : kOutOfRange, 0, 0));
+      s[i] = __builtin_amdgcn_raw_buffer_load_b16(rs, b < nb ? row * 8u + g * 2u : kOutOfRange, 0, 0);
+    }
+  }
+  __device__ __forceinline__ void run(int k0, int k1, int K, const uint32_t (&col)[CT], f32x4 (&acc)[NA][CT]) {
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, end = min(k1, K);
+    if (k0 >= end) return;
+    load_a(k0, end, r, g);
+    for (int k = k0; k < end; k += 256) {
+      u32x4 w[NA][2];
+      float f[NA][2];
+      const int b = k / 32 + g * 2, nb = end / 32;
+#pragma unroll
+      for (int i = 0; i < NA; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          w[i][h] = a[i][h];
+          // a byte past the row's last block says nothing: its codes are zeros, its scale must not be a NaN
+          f[i][h] = mx4_scale(b + h < nb ? s[i] >> (8 * h) & 255u : 127u);
+        }
+      if (k + 256 < end) load_a(k + 256, end, r, g);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        u32x4 x[4][CT][PL];
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          const uint32_t at = b + h < nb && col[c] < kOutOfRange ? col[c] + (b + h) * 64u : kOutOfRange;
+#pragma unroll
+          for (int q = 0; q < PL; ++q)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              x[j][c][q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rc[q], at + j * 16, 0, 0));
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < NA; ++i) {
+            const u32x4 v = mx4_to_bf16(w[i][h][j], f[i][h]);
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+#pragma unroll
+              for (int q = 0; q < PL; ++q) acc[i][c] = mma16<__bf16>(v, x[j][c][q], acc[i][c]);
+          }
+      }
+    }
+  }
+};
+
+// Up: 16 RB values of h per workgroup for one active expert; the waves split the hidden size.
 constexpr int kUpWaves = 4;
-template <typename T, bool MX4>
-__global__ __launch_bounds__(64 * kUpWaves) void moe_up(MoeParams p) {
+template <typename T, bool MX4, int RB, int CTMAX>
+__global__ __launch_bounds__(64 * kUpWaves, 2) void moe_up(MoeParams p) {
   using C = std::conditional_t<MX4, __bf16, T>;
   constexpr bool SPLIT = MX4 && std::is_same_v<T, _Float16>;
-  __shared__ float red[kUpWaves][kMaxTiles][2][64][4];
+  constexpr int PL = SPLIT ? 2 : 1, NA = 2 * RB;
+  __shared__ float red[kUpWaves][NA][64][4];
   __shared__ int32_t token[kMaxTokens];
-  const int slot = blockIdx.y;
-  if (slot >= p.head[0]) return;
-  const int e = p.head[1 + slot];
-  const uint64_t mask = p.masks[slot];
-  const int n = __popcll(mask), tiles = (n + 15) / 16;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
+  const MoeSlot slot = p.slots[blockIdx.y];
+  const int e = __builtin_amdgcn_readfirstlane(slot.expert);
+  if (e < 0) return;
+  const uint64_t mask = slot.mask;
+  const int n = __popcll(mask);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
   if (tid < 64 && (mask >> tid & 1)) token[__popcll(mask & ((1ull << tid) - 1))] = tid;
   __syncthreads();
-  const int f = blockIdx.x * 16 + r;
-  const bool f_ok = f < p.F;
-  const int64_t rows = (int64_t)p.local * 2 * p.F, gate = (int64_t)e * 2 * p.F + f, up = gate + p.F;
-  int64_t xt[kMaxTiles];  // offset of this lane's token in x, or -1
+  const int f0 = blockIdx.x * 16 * RB, rows = min(16 * RB, p.F - f0);
+  const int64_t row0 = (int64_t)e * 2 * p.F + f0;
+  constexpr int KU = MX4 ? 256 : 32;
+  const int units = (p.D + KU - 1) / KU, k0 = units * wave / kUpWaves * KU, k1 = units * (wave + 1) / kUpWaves * KU;
+  const int64_t plane_h = (int64_t)p.T * p.top_k * p.F;
+  auto work = [&](auto ctc) {
+    constexpr int CT = decltype(ctc)::value;
+    uint32_t col[CT];
 #pragma unroll
-  for (int c = 0; c < kMaxTiles; ++c) xt[c] = c * 16 + r < n ? (int64_t)token[c * 16 + r] * p.D : -1;
-  f32x4 acc[kMaxTiles][2] = {};
-  if constexpr (MX4) {
-    const int nb = p.D / 32;
-    const uint16_t *x0 = SPLIT ? p.x_split : p.x, *x1 = p.x_split + (int64_t)p.T * p.D;
-    for (int b0 = wave * 4; b0 < nb; b0 += kUpWaves * 4) {
-      const int b = b0 + g;
-      u32x4 cg = {}, cu = {};
-      float sg = 1, su = 1;
-      if (f_ok && b < nb) {
-        cg = load16(p.gate_up + (gate * nb + b) * 16);
-        cu = load16(p.gate_up + (up * nb + b) * 16);
-        sg = mx4_scale(p.gate_up_s[((b / 8) * rows + gate) * 8 + b % 8]);
-        su = mx4_scale(p.gate_up_s[((b / 8) * rows + up) * 8 + b % 8]);
+    for (int c = 0; c < CT; ++c) col[c] = c * 16 + r < n ? (uint32_t)token[c * 16 + r] * (uint32_t)p.D * 2u : kOutOfRange;
+    f32x4 acc[NA][CT] = {};
+    const uint32_t x_bytes = (uint32_t)p.T * (uint32_t)p.D * 2u;
+    if constexpr (MX4) {
+      Stream4<2, RB, CT, PL> st;
+      st.pitch = (uint32_t)p.D / 2u;
+      st.panel = (int64_t)p.local * 2 * p.F * 8;
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        st.rw[m] = make_rsrc(p.gate_up + (row0 + m * p.F) * st.pitch, rows * st.pitch);
+        st.scales[m] = p.gate_up_s + (row0 + m * p.F) * 8;
+        st.rows[m] = rows;
       }
+      st.rc[0] = make_rsrc(SPLIT ? p.x_split : p.x, x_bytes);
+      if constexpr (SPLIT) st.rc[1] = make_rsrc(p.x_split + (int64_t)p.T * p.D, x_bytes);
+      st.run(k0, k1, p.D, col, acc);
+    } else {
+      Stream16<C, 2, RB, CT, PL> st;
+      st.pitch = (uint32_t)p.D * 2u;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const u32x4 ag = mx4_to_bf16(cg[j], sg), au = mx4_to_bf16(cu[j], su);
-#pragma unroll
-        for (int c = 0; c < kMaxTiles; ++c)
-          if (c < tiles) {
-            u32x4 v = {}, v1 = {};
-            if (xt[c] >= 0 && b < nb) {
-              v = load16(x0 + xt[c] + b * 32 + j * 8);
-              if (SPLIT) v1 = load16(x1 + xt[c] + b * 32 + j * 8);
-            }
-            acc[c][0] = mma16<C>(ag, v, acc[c][0]);
-            acc[c][1] = mma16<C>(au, v, acc[c][1]);
-            if (SPLIT) {
-              acc[c][0] = mma16<C>(ag, v1, acc[c][0]);
-              acc[c][1] = mma16<C>(au, v1, acc[c][1]);
-            }
-          }
-      }
+      for (int m = 0; m < 2; ++m) st.rw[m] = make_rsrc(p.gate_up + (row0 + m * p.F) * st.pitch, rows * st.pitch);
+      st.rc[0] = make_rsrc(p.x, x_bytes);
+      st.run(k0, k1, p.D, col, acc);
     }
-  } else {
-    const uint16_t *w = reinterpret_cast<const uint16_t *>(p.gate_up);
-    for (int k0 = wave * 32; k0 < p.D; k0 += kUpWaves * 32) {
-      const int k = k0 + g * 8;
-      u32x4 ag = {}, au = {};
-      if (f_ok && k < p.D) {
-        ag = load16(w + gate * p.D + k);
-        au = load16(w + up * p.D + k);
-      }
 #pragma unroll
-      for (int c = 0; c < kMaxTiles; ++c)
-        if (c < tiles) {
-          u32x4 v = {};
-          if (xt[c] >= 0 && k < p.D) v = load16(p.x + xt[c] + k);
-          acc[c][0] = mma16<C>(ag, v, acc[c][0]);
-          acc[c][1] = mma16<C>(au, v, acc[c][1]);
+    for (int c = 0; c < CT; ++c) {
+      if (c) __syncthreads();
+#pragma unroll
+      for (int i = 0; i < NA; ++i) *reinterpret_cast<f32x4 *>(red[wave][i][lane]) = acc[i][c];
+      __syncthreads();
+      // value (row block b, f, column): f fastest, so that neighbours write neighbours
+      for (int i = tid; i < RB * 256; i += 64 * kUpWaves) {
+        const int q = i & 3, gg = (i >> 2) & 3, b = (i >> 4) % RB, cc = i / (16 * RB), l = gg * 16 + cc;
+        const int column = c * 16 + cc, ff = f0 + b * 16 + gg * 4 + q;
+        if (column >= n || ff >= p.F) continue;
+        float a = 0, u = 0;
+#pragma unroll
+        for (int w = 0; w < kUpWaves; ++w) {
+          a += red[w][b][l][q];
+          u += red[w][RB + b][l][q];
         }
+        const float v = a / (1.0f + __expf(-a)) * u;
+        const int64_t at = (int64_t)(slot.row + column) * p.F + ff;
+        const C hi = (C)v;
+        const C lo = fabsf((float)hi) < __builtin_inff() ? (C)(v - (float)hi) : (C)0.0f;
+        reinterpret_cast<C *>(p.h)[at] = hi;
+        reinterpret_cast<C *>(p.h)[plane_h + at] = lo;
+      }
     }
-  }
-#pragma unroll
-  for (int c = 0; c < kMaxTiles; ++c)
-    for (int q = 0; q < 2; ++q) *reinterpret_cast<f32x4 *>(red[wave][c][q][lane]) = acc[c][q];
-  __syncthreads();
-  const int64_t plane = (int64_t)p.T * p.top_k * p.F;
-  for (int i = tid; i < tiles * 256; i += 64 * kUpWaves) {
-    const int c = i >> 8, l = (i >> 2) & 63, q = i & 3, col = c * 16 + (l & 15), ff = blockIdx.x * 16 + (l >> 4) * 4 + q;
-    if (col >= n || ff >= p.F) continue;
-    float a = 0, b = 0;
-    for (int w = 0; w < kUpWaves; ++w) {
-      a += red[w][c][0][l][q];
-      b += red[w][c][1][l][q];
-    }
-    const float v = a / (1.0f + __expf(-a)) * b;
-    const int t = token[col];
-    int j = 0;
-    while (j < p.top_k - 1 && p.ids[t * p.top_k + j] != p.first + e) ++j;
-    const int64_t at = (int64_t)(t * p.top_k + j) * p.F + ff;
-    const C hi = (C)v;
-    const C lo = fabsf((float)hi) < __builtin_inff() ? (C)(v - (float)hi) : (C)0.0f;
-    reinterpret_cast<C *>(p.h)[at] = hi;
-    reinterpret_cast<C *>(p.h)[plane + at] = lo;
+  };
+  using std::integral_constant;
+  if (CTMAX == 1 || n <= 16) work(integral_constant<int, 1>{});
+  else if constexpr (CTMAX > 1) {
+    if (CTMAX == 2 || n <= 32) work(integral_constant<int, 2>{});
+    else if constexpr (CTMAX > 2) work(integral_constant<int, 4>{});
   }
 }
 
-// Down: 16 outputs of every token per workgroup; its waves share the active
-// experts' ffn evenly (in units of 128 values, an expert after the other).
-constexpr int kDownWaves = 8, kUnit = 128;
-template <typename T, bool MX4>
-__global__ __launch_bounds__(64 * kDownWaves) void moe_down(MoeParams p) {
+// Down: 16 RB outputs of every token per workgroup; the waves of `splits`
+// workgroups share the active experts' ffn evenly, an expert after the other.
+constexpr int kDownWaves = 8;
+template <typename T, bool MX4, int RB, int CTMAX>
+__global__ __launch_bounds__(64 * kDownWaves, 2) void moe_down(MoeParams p) {
   using C = std::conditional_t<MX4, __bf16, T>;
-  __shared__ float red[kDownWaves][kMaxTiles][64][4];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
-  const int d = blockIdx.x * 16 + r, tiles = (p.T + 15) / 16;
-  const bool d_ok = d < p.D;
-  const int units = (p.F + kUnit - 1) / kUnit;
-  const int64_t total = (int64_t)p.head[0] * units, rows = (int64_t)p.local * p.D;
-  int64_t u = total * wave / kDownWaves;
-  const int64_t u_end = total * (wave + 1) / kDownWaves, plane = (int64_t)p.T * p.top_k * p.F;
-  f32x4 sum[kMaxTiles] = {};
+  __shared__ float red[kDownWaves][RB][64][4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
+  const int d0 = blockIdx.x * 16 * RB, rows = min(16 * RB, p.D - d0);
+  constexpr int KU = MX4 ? 256 : 128;
+  const int units = (p.F + KU - 1) / KU;
+  const int64_t total = (int64_t)p.head[0] * units;
+  const int part = blockIdx.y * kDownWaves + wave, parts = p.splits * kDownWaves;
+  int64_t u = total * part / parts;
+  const int64_t u_end = total * (part + 1) / parts, plane = (int64_t)p.T * p.top_k * p.F;
+  const uint32_t h_bytes = (uint32_t)(plane * 2);
+  f32x4 sum[RB][CTMAX] = {};
   while (u < u_end) {
-    const int slot = (int)(u / units), first = (int)(u % units);
+    const int at = (int)(u / units), first = (int)(u - (int64_t)at * units);
     const int last = (int)min((int64_t)units, first + (u_end - u));
     u += last - first;
-    const int e = p.head[1 + slot];
-    const uint64_t mask = p.masks[slot];
-    const int64_t row = (int64_t)e * p.D + d;
-    f32x4 acc[kMaxTiles] = {};
-    int64_t ht[kMaxTiles];  // offset of this lane's token's h, or -1
-    float wt[kMaxTiles];
+    const MoeSlot slot = p.slots[at];
+    const int e = __builtin_amdgcn_readfirstlane(slot.expert), n = __popcll(slot.mask);
+    const int64_t row0 = (int64_t)e * p.D + d0;
+    // CT tiles of columns; with CTMAX == 1 column r is token r, otherwise the
+    // expert's tokens from the one of rank `base` on are packed into the columns
+    auto work = [&](auto ctc, int base) {
+      constexpr int CT = decltype(ctc)::value;
+      uint32_t col[CT];
 #pragma unroll
-    for (int c = 0; c < kMaxTiles; ++c) {
-      const int t = c * 16 + r;
-      ht[c] = -1;
-      wt[c] = 0;
-      if (mask >> t & 1) {
-        int j = 0;
-        while (j < p.top_k - 1 && p.ids[t * p.top_k + j] != p.first + e) ++j;
-        ht[c] = (int64_t)(t * p.top_k + j) * p.F;
-        wt[c] = p.wts[t * p.top_k + j];
+      for (int c = 0; c < CT; ++c) {
+        const int rank = CTMAX == 1 ? __popcll(slot.mask & ((1ull << r) - 1)) : base + c * 16 + r;
+        const bool has = CTMAX == 1 ? slot.mask >> r & 1 : rank < n;
+        col[c] = has ? (uint32_t)(slot.row + rank) * (uint32_t)p.F * 2u : kOutOfRange;
       }
-    }
-    if constexpr (MX4) {
-      const int nb = p.F / 32;
-      for (int b0 = first * 4; b0 < last * 4; b0 += 4) {
-        const int b = b0 + g;
-        u32x4 cd = {};
-        float sd = 1;
-        if (d_ok && b < nb) {
-          cd = load16(p.down + (row * nb + b) * 16);
-          sd = mx4_scale(p.down_s[((b / 8) * rows + row) * 8 + b % 8]);
-        }
+      f32x4 acc[RB][CT] = {};
+      if constexpr (MX4) {
+        Stream4<1, RB, CT, 2> st;
+        st.pitch = (uint32_t)p.F / 2u;
+        st.panel = (int64_t)p.local * p.D * 8;
+        st.rw[0] = make_rsrc(p.down + row0 * st.pitch, rows * st.pitch);
+        st.scales[0] = p.down_s + row0 * 8;
+        st.rows[0] = rows;
+        st.rc[0] = make_rsrc(p.h, h_bytes);
+        st.rc[1] = make_rsrc(p.h + plane, h_bytes);
+        st.run(first * KU, last * KU, p.F, col, acc);
+      } else {
+        Stream16<C, 1, RB, CT, 2> st;
+        st.pitch = (uint32_t)p.F * 2u;
+        st.rw[0] = make_rsrc(p.down + row0 * st.pitch, rows * st.pitch);
+        st.rc[0] = make_rsrc(p.h, h_bytes);
+        st.rc[1] = make_rsrc(p.h + plane, h_bytes);
+        st.run(first * KU, last * KU, p.F, col, acc);
+      }
+      // only the expert's own tokens: a NaN or an infinity in its weights stays with them
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const u32x4 a = mx4_to_bf16(cd[j], sd);
+      for (int c = 0; c < CTMAX; ++c) {
+        const int t = c * 16 + r, rank = __popcll(slot.mask & ((1ull << t) - 1)), pos = rank - base;
+        const bool mine = (slot.mask >> t & 1) && pos >= 0 && pos < CT * 16;
+        const float w = mine ? p.row_w[slot.row + rank] : 0.0f;
 #pragma unroll
-          for (int c = 0; c < kMaxTiles; ++c)
-            if (mask >> (c * 16) & 0xFFFF) {
-              u32x4 hi = {}, lo = {};
-              if (ht[c] >= 0 && b < nb) {
-                hi = load16(p.h + ht[c] + b * 32 + j * 8);
-                lo = load16(p.h + plane + ht[c] + b * 32 + j * 8);
+        for (int i = 0; i < RB; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float v = acc[i][0][q];
+            if constexpr (CTMAX > 1) {
+              const int from = (pos & 15) + g * 16;
+              v = __shfl(acc[i][0][q], from);
+              if constexpr (CT > 1) {
+                const float o = __shfl(acc[i][1][q], from);
+                v = pos >= 16 ? o : v;
               }
-              acc[c] = mma16<C>(a, hi, acc[c]);
-              acc[c] = mma16<C>(a, lo, acc[c]);
             }
-        }
-      }
-    } else {
-      const uint16_t *w = reinterpret_cast<const uint16_t *>(p.down);
-      for (int k0 = first * kUnit; k0 < last * kUnit && k0 < p.F; k0 += 32) {
-        const int k = k0 + g * 8;
-        u32x4 a = {};
-        if (d_ok && k < p.F) a = load16(w + row * p.F + k);
-#pragma unroll
-        for (int c = 0; c < kMaxTiles; ++c)
-          if (mask >> (c * 16) & 0xFFFF) {
-            u32x4 hi = {}, lo = {};
-            if (ht[c] >= 0 && k < p.F) {
-              hi = load16(p.h + ht[c] + k);
-              lo = load16(p.h + plane + ht[c] + k);
-            }
-            acc[c] = mma16<C>(a, hi, acc[c]);
-            acc[c] = mma16<C>(a, lo, acc[c]);
+            if (mine) sum[i][c][q] += w * v;
           }
       }
+    };
+    using std::integral_constant;
+    if (CTMAX == 1 || n <= 16) {
+      work(integral_constant<int, 1>{}, 0);
+    } else if constexpr (CTMAX > 1) {
+      // past 32 tokens of one expert its rows are read again, now from cache
+      for (int base = 0; base < n; base += 32) work(integral_constant<int, 2>{}, base);
     }
-    // only the expert's own tokens: a NaN or an infinity in its weights stays with them
-#pragma unroll
-    for (int c = 0; c < kMaxTiles; ++c)
-      if (ht[c] >= 0)
-        for (int q = 0; q < 4; ++q) sum[c][q] += wt[c] * acc[c][q];
   }
 #pragma unroll
-  for (int c = 0; c < kMaxTiles; ++c) *reinterpret_cast<f32x4 *>(red[wave][c][lane]) = sum[c];
-  __syncthreads();
-  for (int i = tid; i < tiles * 256; i += 64 * kDownWaves) {
-    const int c = i >> 8, l = (i >> 2) & 63, q = i & 3, t = c * 16 + (l & 15), dd = blockIdx.x * 16 + (l >> 4) * 4 + q;
-    if (t >= p.T || dd >= p.D) continue;
-    float s = 0;
-    for (int w = 0; w < kDownWaves; ++w) s += red[w][c][l][q];
-    reinterpret_cast<T *>(p.out)[(int64_t)t * p.D + dd] = (T)s;
+  for (int c = 0; c < CTMAX; ++c) {
+    if (c) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < RB; ++i) *reinterpret_cast<f32x4 *>(red[wave][i][lane]) = sum[i][c];
+    __syncthreads();
+    for (int i = tid; i < RB * 256; i += 64 * kDownWaves) {
+      const int q = i & 3, gg = (i >> 2) & 3, b = (i >> 4) % RB, cc = i / (16 * RB), l = gg * 16 + cc;
+      const int t = c * 16 + cc, d = d0 + b * 16 + gg * 4 + q;
+      if (t >= p.T || d >= p.D) continue;
+      float v = 0;
+#pragma unroll
+      for (int w = 0; w < kDownWaves; ++w) v += red[w][b][l][q];
+      if (p.splits == 1)
+        reinterpret_cast<T *>(p.out)[(int64_t)t * p.D + d] = (T)v;
+      else
+        put(&p.partial[((int64_t)blockIdx.y * p.T + t) * p.D + d], v);
+    }
+  }
+  if (p.splits == 1) return;
+  // the last of the tile's workgroups adds the parts up, in their order
+  if (!arrive_last(&p.counters[8 + blockIdx.x], p.splits)) return;
+  for (int i = tid; i < p.T * 16 * RB; i += 64 * kDownWaves) {
+    const int t = i / (16 * RB), d = d0 + i % (16 * RB);
+    if (d >= p.D) continue;
+    float v = 0;
+    for (int s = 0; s < p.splits; ++s) v += get(&p.partial[((int64_t)s * p.T + t) * p.D + d]);
+    reinterpret_cast<T *>(p.out)[(int64_t)t * p.D + d] = (T)v;
   }
 }
 
-template <typename T, bool MX4>
-int launch_typed(const MoeParams &p, hipStream_t s) {
+template <typename T, bool MX4, int RBU, int RBD, int CT>
+int launch_sized(MoeParams p, int cus, hipStream_t s) {
   constexpr bool SPLIT = MX4 && std::is_same_v<T, _Float16>;
-  const int split = SPLIT ? (int)(((int64_t)p.T * p.D + 64 * kRouterWaves * 8 - 1) / (64 * kRouterWaves * 8)) : 0;
-  moe_router<T><<<p.router_wgs + split, 64 * kRouterWaves, 0, s>>>(p);
+  const int split = SPLIT ? (int)(((int64_t)p.T * p.D + 64 * kRouterWaves * 4 - 1) / (64 * kRouterWaves * 4)) : 0;
+  moe_router<T><<<p.expert_wgs * p.tiles + split, 64 * kRouterWaves, 0, s>>>(p);
   if (hipGetLastError() != hipSuccess) return FO_ERR_HIP;
-  const int most = p.local < p.T * p.top_k ? p.local : p.T * p.top_k;  // experts that can be active
-  moe_up<T, MX4><<<dim3((p.F + 15) / 16, most), 64 * kUpWaves, 0, s>>>(p);
+  moe_up<T, MX4, RBU, CT><<<dim3((p.F + 16 * RBU - 1) / (16 * RBU), p.most), 64 * kUpWaves, 0, s>>>(p);
   if (hipGetLastError() != hipSuccess) return FO_ERR_HIP;
-  moe_down<T, MX4><<<(p.D + 15) / 16, 64 * kDownWaves, 0, s>>>(p);
+  // enough workgroups for two a CU, as long as every wave has a few steps of K
+  const int tiles = (p.D + 16 * RBD - 1) / (16 * RBD), units = (p.F + 255) / 256;
+  int splits = (2 * cus + tiles - 1) / tiles;
+  const int64_t most = (int64_t)p.most * units / (kDownWaves * 2);
+  if (splits > most) splits = (int)most;
+  if (splits > kMoeMaxSplits) splits = kMoeMaxSplits;
+  p.splits = splits < 1 ? 1 : splits;
+  moe_down<T, MX4, RBD, CT><<<dim3(tiles, p.splits), 64 * kDownWaves, 0, s>>>(p);
   return hipGetLastError() == hipSuccess ? FO_OK : FO_ERR_HIP;
+}
+
+template <typename T, bool MX4>
+int launch_typed(const MoeParams &p, int cus, hipStream_t s) {
+  if (p.T <= 4) return launch_sized<T, MX4, 1, 1, 1>(p, cus, s);
+  if (p.T <= 16) return launch_sized<T, MX4, 2, 4, 1>(p, cus, s);
+  if (p.T <= 32) return launch_sized<T, MX4, 2, 4, 2>(p, cus, s);
+  return launch_sized<T, MX4, 2, 4, 4>(p, cus, s);
 }
 
 }  // namespace
@@ -435,14 +684,16 @@ int launch_moe(const fo_moe_desc &d, int32_t tokens, const void *x, const void *
   p.out = static_cast<uint16_t *>(out);
   p.ids_out = ids;
   p.wts_out = weights;
-  p.counter = reinterpret_cast<uint32_t *>(ws + l.counter);
+  p.counters = reinterpret_cast<uint32_t *>(ws + l.counters);
   p.head = reinterpret_cast<int32_t *>(ws + l.head);
-  p.masks = reinterpret_cast<uint64_t *>(ws + l.masks);
+  p.slots = reinterpret_cast<MoeSlot *>(ws + l.slots);
+  p.row_w = reinterpret_cast<float *>(ws + l.row_w);
   p.ids = reinterpret_cast<int32_t *>(ws + l.ids);
   p.wts = reinterpret_cast<float *>(ws + l.wts);
   p.logits = reinterpret_cast<float *>(ws + l.logits);
   p.x_split = reinterpret_cast<uint16_t *>(ws + l.x_split);
   p.h = reinterpret_cast<uint16_t *>(ws + l.h);
+  p.partial = reinterpret_cast<float *>(ws + l.partial);
   p.T = tokens;
   p.D = (int32_t)d.hidden;
   p.F = (int32_t)d.ffn;
@@ -451,10 +702,12 @@ int launch_moe(const fo_moe_desc &d, int32_t tokens, const void *x, const void *
   p.first = d.first_expert;
   p.local = d.local_experts;
   p.renorm = d.renormalize;
-  p.router_wgs = (d.experts + 15) / 16;
+  p.expert_wgs = (d.experts + 15) / 16;
+  p.tiles = (tokens + 15) / 16;
+  p.most = p.local < p.T * p.top_k ? p.local : p.T * p.top_k;  // experts that can be active
   if (d.weights == FO_MOE_MX4)
-    return d.dtype == FO_BF16 ? launch_typed<__bf16, true>(p, s) : launch_typed<_Float16, true>(p, s);
-  return d.dtype == FO_BF16 ? launch_typed<__bf16, false>(p, s) : launch_typed<_Float16, false>(p, s);
+    return d.dtype == FO_BF16 ? launch_typed<__bf16, true>(p, cus, s) : launch_typed<_Float16, true>(p, cus, s);
+  return d.dtype == FO_BF16 ? launch_typed<__bf16, false>(p, cus, s) : launch_typed<_Float16, false>(p, cus, s);
 }
 
 }  // namespace fo

@@ -17,16 +17,21 @@ int launch_mx4_gemm(const void *a_codes, const void *a_scales, const void *b_cod
                     int64_t M, int64_t N, int64_t K, int32_t dtype, int32_t problems, const int32_t *row_ends,
                     int cus, hipStream_t s);
 
+// Most workgroups that share one tile of a layer's outputs.
+constexpr int kMoeMaxSplits = 16;
+
 // Parts of a layer's workspace, as byte offsets; each begins on 256 bytes.
 struct MoeLayout {
-  int64_t counter;   // u32: router workgroups done; zero between calls
-  int64_t head;      // int32: number of active experts, then their local indices [local_experts]
-  int64_t masks;     // u64 [local_experts]: the tokens of each active expert
+  int64_t counters;  // u32 [8 + outputs / 16]: workgroups done; zero between calls
+  int64_t head;      // int32: number of active experts
+  int64_t slots;     // 16 bytes for each expert that can be active
+  int64_t row_w;     // float [max_tokens * top_k]: weight of each row of h
   int64_t ids;       // int32 [max_tokens][top_k]: picked experts
   int64_t wts;       // float [max_tokens][top_k]: their weights
   int64_t logits;    // float [max_tokens][experts]
   int64_t x_split;   // bf16 [2][max_tokens][hidden]: fp16 tokens as two bf16 values (4-bit weights only)
   int64_t h;         // 16-bit [2][max_tokens * top_k][ffn]: the activations as pairs
+  int64_t partial;   // float [kMoeMaxSplits][max_tokens][hidden]
   int64_t bytes;
 };
 inline MoeLayout moe_layout(const fo_moe_desc &d) {
@@ -37,14 +42,17 @@ inline MoeLayout moe_layout(const fo_moe_desc &d) {
     at += (bytes + 255) / 256 * 256;
     return here;
   };
-  l.counter = take(4);
-  l.head = take(4 * (1 + (int64_t)d.local_experts));
-  l.masks = take(8 * (int64_t)d.local_experts);
-  l.ids = take(4 * (int64_t)d.max_tokens * d.top_k);
-  l.wts = take(4 * (int64_t)d.max_tokens * d.top_k);
+  const int64_t picks = (int64_t)d.max_tokens * d.top_k;
+  l.counters = take(4 * (8 + (d.hidden + 15) / 16));
+  l.head = take(4);
+  l.slots = take(16 * (picks < d.local_experts ? picks : d.local_experts));
+  l.row_w = take(4 * picks);
+  l.ids = take(4 * picks);
+  l.wts = take(4 * picks);
   l.logits = take(4 * (int64_t)d.max_tokens * d.experts);
   l.x_split = take(d.weights == FO_MOE_MX4 && d.dtype == FO_FP16 ? 4 * d.max_tokens * d.hidden : 0);
-  l.h = take(4 * (int64_t)d.max_tokens * d.top_k * d.ffn);
+  l.h = take(4 * picks * d.ffn);
+  l.partial = take(4 * (int64_t)kMoeMaxSplits * d.max_tokens * d.hidden);
   l.bytes = at;
   return l;
 }
