@@ -41,8 +41,8 @@ struct MoeParams {
   int32_t *ids;
   float *wts;
   float *logits;
-  uint16_t *x_split;   // [2][tokens][D]
-  uint16_t *h;         // [2][rows][F]
+  uint16_t *x_panels;  // [tokens][1 or 2][panels of D]: the tokens as 4-bit weights meet them
+  uint16_t *h;         // [rows][2][F, or panels of F]
   float *partial;      // [splits][T][D]
   int32_t T, D, F, E, top_k, first, local, renorm, expert_wgs, tiles, most, splits;
 };
@@ -68,6 +68,20 @@ __device__ __forceinline__ u32x4 mx4_to_bf16(uint32_t codes, float scale) {
   v[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 2));
   v[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 3));
   return v;
+}
+
+__device__ __forceinline__ u32x4 load16(const void *p) { return *reinterpret_cast<const u32x4 *>(p); }
+
+// Columns that meet 4-bit weights lie in panels of 256 values, ordered as the
+// lanes read them: chunk (half h, dword j) of lane group g, which is values
+// 8 j .. 8 j + 7 of block 2 g + h, at place (4 h + j) * 4 + g.  The four groups of a
+// load then read 64 neighbouring bytes of a column; in the values' own order
+// they would read 16 bytes of each of four blocks, and four loads would each
+// bring the same lines.
+__host__ __device__ __forceinline__ int64_t panels_of(int64_t k) { return (k + 255) / 256 * 256; }
+__device__ __forceinline__ int panel_place(int k) {
+  const int g = k >> 6 & 3, h = k >> 5 & 1, j = k >> 3 & 3;
+  return (k & ~255) + ((h * 4 + j) * 4 + g) * 8 + (k & 7);
 }
 
 // Order of the logits as unsigned integers: a NaN above every number, -0 as +0; 0 is below all.
@@ -198,15 +212,28 @@ __global__ __launch_bounds__(64 * kRouterWaves) void moe_router(MoeParams p) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
   constexpr int kThreads = 64 * kRouterWaves;
   const int wgs = p.expert_wgs * p.tiles;
-  if ((int)blockIdx.x >= wgs) {  // the workgroups that split fp16 tokens into two bf16 values
-    const int64_t n = (int64_t)p.T * p.D, step = (int64_t)(gridDim.x - wgs) * kThreads;
-    for (int64_t i = (int64_t)(blockIdx.x - wgs) * kThreads + tid; i < n; i += step) {
-      const float v = (float)reinterpret_cast<const T *>(p.x)[i];
-      const __bf16 hi = (__bf16)v;
-      // an infinity or a NaN goes whole into the first part
-      const __bf16 lo = fabsf(v) < __builtin_inff() ? (__bf16)(v - (float)hi) : (__bf16)0.0f;
-      reinterpret_cast<__bf16 *>(p.x_split)[i] = hi;
-      reinterpret_cast<__bf16 *>(p.x_split)[n + i] = lo;
+  if ((int)blockIdx.x >= wgs) {  // the workgroups that lay the tokens out for 4-bit weights
+    constexpr bool PAIR = std::is_same_v<T, _Float16>;
+    const int chunks = p.D / 8, n = p.T * chunks, step = (gridDim.x - wgs) * kThreads;
+    const int64_t row = panels_of(p.D);
+    for (int i = (blockIdx.x - wgs) * kThreads + tid; i < n; i += step) {
+      const int t = i / chunks, d = (i - t * chunks) * 8;
+      const u32x4 v = load16(p.x + (int64_t)t * p.D + d);
+      uint16_t *to = p.x_panels + t * row * (PAIR ? 2 : 1) + panel_place(d);
+      if constexpr (PAIR) {  // an fp16 value as two bf16 values
+        const f16x8 f = __builtin_bit_cast(f16x8, v);
+        bf16x8 hi, lo;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          hi[q] = (__bf16)(float)f[q];
+          // an infinity or a NaN goes whole into the first one
+          lo[q] = fabsf((float)f[q]) < __builtin_inff() ? (__bf16)((float)f[q] - (float)hi[q]) : (__bf16)0.0f;
+        }
+        *reinterpret_cast<bf16x8 *>(to) = hi;
+        *reinterpret_cast<bf16x8 *>(to + row) = lo;
+      } else {
+        *reinterpret_cast<u32x4 *>(to) = v;
+      }
     }
     return;
   }
@@ -317,14 +344,15 @@ __global__ __launch_bounds__(64 * kRouterWaves) void moe_router(MoeParams p) {
   }
 }
 
-// Weights of PARTS matrices (RB blocks of 16 rows each) times CT tiles of
-// columns that come in PL parts (1, or 2 whose sum is meant), over k in
-// [k0, k1): k0 a multiple of 32 (256 with 4-bit weights), K the row length.
-// col[c]: byte offset of this lane's column in every part; out of range: none.
-template <typename C, int PARTS, int RB, int CT, int PL>
+// Rows of PARTS matrices (RB blocks of 16 rows each) times CT tiles of 16
+// columns, over k in [k0, k1): k0 a multiple of 32 (256 with 4-bit weights), K
+// the row length.  col[c]: byte offset of this lane's column, kOutOfRange: none.
+// `rot` says which group of K comes first: workgroups that begin at different
+// places spread over the memory channels (rows lie a power of two apart).
+template <typename C, int PARTS, int RB, int CT>
 struct Stream16 {
   static constexpr int NA = PARTS * RB, U = NA >= 8 ? 1 : 8 / NA;
-  __amdgpu_buffer_rsrc_t rw[PARTS], rc[PL];
+  __amdgpu_buffer_rsrc_t rw[PARTS], rc;
   uint32_t pitch;
   u32x4 a[U][NA];
   __device__ __forceinline__ void load_a(int k, int end, int r, int g) {
@@ -338,34 +366,32 @@ struct Stream16 {
       }
     }
   }
-  __device__ __forceinline__ void run(int k0, int k1, int K, const uint32_t (&col)[CT], f32x4 (&acc)[NA][CT]) {
+  __device__ __forceinline__ void run(int k0, int k1, int K, int rot, const uint32_t (&col)[CT], f32x4 (&acc)[NA][CT]) {
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, end = min(k1, K);
     if (k0 >= end) return;
-    load_a(k0, end, r, g);
-    for (int k = k0; k < end; k += U * 32) {
-      u32x4 b[U][CT][PL], w[U][NA];
+    const int groups = (end - k0 + U * 32 - 1) / (U * 32);
+    int group = rot % groups;
+    load_a(k0 + group * U * 32, end, r, g);
+    for (int n = 0; n < groups; ++n) {
+      u32x4 x[U][CT], w[U][NA];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int kk = k + u * 32 + g * 8;
+        const int kk = k0 + (group * U + u) * 32 + g * 8;
 #pragma unroll
-        for (int c = 0; c < CT; ++c) {
-          const uint32_t at = kk < end && col[c] < kOutOfRange ? col[c] + kk * 2u : kOutOfRange;
-#pragma unroll
-          for (int q = 0; q < PL; ++q)
-            b[u][c][q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rc[q], at, 0, 0));
-        }
+        for (int c = 0; c < CT; ++c)
+          x[u][c] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                  rc, kk < end && col[c] < kOutOfRange ? col[c] + kk * 2u : kOutOfRange, 0, 0));
 #pragma unroll
         for (int i = 0; i < NA; ++i) w[u][i] = a[u][i];
       }
-      load_a(k + U * 32, end, r, g);
+      if (++group == groups) group = 0;
+      if (n + 1 < groups) load_a(k0 + group * U * 32, end, r, g);
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int c = 0; c < CT; ++c)
 #pragma unroll
-          for (int q = 0; q < PL; ++q)
-#pragma unroll
-            for (int i = 0; i < NA; ++i) acc[i][c] = mma16<C>(w[u][i], b[u][c][q], acc[i][c]);
+          for (int i = 0; i < NA; ++i) acc[i][c] = mma16<C>(w[u][i], x[u][c], acc[i][c]);
     }
   }
 };
@@ -373,10 +399,10 @@ struct Stream16 {
 // The same with 4-bit weights.  A step is a panel of 8 blocks: lane group g takes
 // blocks 2 g and 2 g + 1 of it, so that its codes are 32 and its scales 2
 // neighbouring bytes (the order of k is free as long as the columns follow it).
-template <int PARTS, int RB, int CT, int PL>
+template <int PARTS, int RB, int CT>
 struct Stream4 {
   static constexpr int NA = PARTS * RB;
-  __amdgpu_buffer_rsrc_t rw[PARTS], rc[PL];
+  __amdgpu_buffer_rsrc_t rw[PARTS], rc;
   const uint8_t *scales[PARTS];  // of the part's first row, panel 0
   int64_t panel;                 // bytes of a panel
   uint32_t rows[PARTS];          // rows of the part from its first one on
@@ -396,81 +422,122 @@ struct Stream4 {
       s[i] = __builtin_amdgcn_raw_buffer_load_b16(rs, b < nb ? row * 8u + g * 2u : kOutOfRange, 0, 0);
     }
   }
-  __device__ __forceinline__ void run(int k0, int k1, int K, const uint32_t (&col)[CT], f32x4 (&acc)[NA][CT]) {
-    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, end = min(k1, K);
-    if (k0 >= end) return;
-    load_a(k0, end, r, g);
-    for (int k = k0; k < end; k += 256) {
-      u32x4 w[NA][2];
-      float f[NA][2];
-      const int b = k / 32 + g * 2, nb = end / 32;
+  // the columns' values of one half (lane group g's block 2 g + h) of the panel at k, in panel_place order
+  __device__ __forceinline__ void load_x(u32x4 (&x)[4][CT], int k, int h, int end, int g, const uint32_t (&col)[CT]) {
+    const int b = k / 32 + g * 2 + h;
 #pragma unroll
-      for (int i = 0; i < NA; ++i)
+    for (int c = 0; c < CT; ++c) {
+      const uint32_t at = b < end / 32 && col[c] < kOutOfRange ? col[c] + k * 2u + h * 256u + g * 16u : kOutOfRange;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          w[i][h] = a[i][h];
-          // a byte past the row's last block says nothing: its codes are zeros, its scale must not be a NaN
-          f[i][h] = mx4_scale(b + h < nb ? s[i] >> (8 * h) & 255u : 127u);
-        }
-      if (k + 256 < end) load_a(k + 256, end, r, g);
+      for (int j = 0; j < 4; ++j)
+        x[j][c] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rc, at + j * 64, 0, 0));
+    }
+  }
+  __device__ __forceinline__ void multiply(const u32x4 (&w)[NA], const float (&f)[NA], const u32x4 (&x)[4][CT],
+                                           f32x4 (&acc)[NA][CT]) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        u32x4 x[4][CT][PL];
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int c = 0; c < CT; ++c) {
-          const uint32_t at = b + h < nb && col[c] < kOutOfRange ? col[c] + (b + h) * 64u : kOutOfRange;
+      for (int i = 0; i < NA; ++i) {
+        const u32x4 v = mx4_to_bf16(w[i][j], f[i]);
 #pragma unroll
-          for (int q = 0; q < PL; ++q)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              x[j][c][q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rc[q], at + j * 16, 0, 0));
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int i = 0; i < NA; ++i) {
-            const u32x4 v = mx4_to_bf16(w[i][h][j], f[i][h]);
-#pragma unroll
-            for (int c = 0; c < CT; ++c)
-#pragma unroll
-              for (int q = 0; q < PL; ++q) acc[i][c] = mma16<__bf16>(v, x[j][c][q], acc[i][c]);
-          }
+        for (int c = 0; c < CT; ++c) acc[i][c] = mma16<__bf16>(v, x[j][c], acc[i][c]);
       }
+  }
+  // Loads return in order, so the columns of a panel (from cache) are asked for
+  // before the next panel's weights (from memory): waiting for them then does
+  // not wait for the weights.
+  __device__ __forceinline__ void run(int k0, int k1, int K, int rot, const uint32_t (&col)[CT], f32x4 (&acc)[NA][CT]) {
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, end = min(k1, K), nb = end / 32;
+    if (k0 >= end) return;
+    const int groups = (end - k0 + 255) / 256;
+    int group = rot % groups;
+    load_a(k0 + group * 256, end, r, g);
+    for (int n = 0; n < groups; ++n) {
+      u32x4 w0[NA], w1[NA], x0[4][CT], x1[4][CT];
+      float f0[NA], f1[NA];
+      const int k = k0 + group * 256, b = k / 32 + g * 2;
+      load_x(x0, k, 0, end, g, col);
+      if constexpr (CT <= 2) load_x(x1, k, 1, end, g, col);
+#pragma unroll
+      for (int i = 0; i < NA; ++i) {
+        w0[i] = a[i][0];
+        w1[i] = a[i][1];
+        // a byte past the row's last block says nothing: its codes are zeros, its scale must not be a NaN
+        f0[i] = mx4_scale(b < nb ? s[i] & 255u : 127u);
+        f1[i] = mx4_scale(b + 1 < nb ? s[i] >> 8 : 127u);
+      }
+      if constexpr (CT > 2) {
+        multiply(w0, f0, x0, acc);
+        load_x(x1, k, 1, end, g, col);
+      }
+      if (++group == groups) group = 0;
+      if (n + 1 < groups) load_a(k0 + group * 256, end, r, g);
+      if constexpr (CT <= 2) multiply(w0, f0, x0, acc);
+      multiply(w1, f1, x1, acc);
     }
   }
 };
+
+// Tokens that come as pairs of 16-bit values (whose sum is meant) take two
+// columns each, the first values in the lower half of the columns: 8 tokens fit
+// one tile, so that a few tokens need one product and one load where two
+// products of 16 columns would mostly multiply zeros.  fold() adds the halves up.
+template <int CT>
+constexpr int kPairTokens = CT * 8;
+template <int NA, int CT>
+__device__ __forceinline__ void fold(f32x4 (&acc)[NA][CT]) {
+#pragma unroll
+  for (int i = 0; i < NA; ++i) {
+    if constexpr (CT == 1) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)  // columns r and r + 8 of a row of 16 lanes
+        acc[i][0][q] += __uint_as_float(moved<0x128>(__float_as_uint(acc[i][0][q]), 0));
+    } else {
+#pragma unroll
+      for (int c = 0; c < CT / 2; ++c) acc[i][c] += acc[i][c + CT / 2];
+    }
+  }
+}
 
 // Up: 16 RB values of h per workgroup for one active expert; the waves split the hidden size.
 constexpr int kUpWaves = 4;
 template <typename T, bool MX4, int RB, int CTMAX>
 __global__ __launch_bounds__(64 * kUpWaves, 2) void moe_up(MoeParams p) {
   using C = std::conditional_t<MX4, __bf16, T>;
-  constexpr bool SPLIT = MX4 && std::is_same_v<T, _Float16>;
-  constexpr int PL = SPLIT ? 2 : 1, NA = 2 * RB;
+  constexpr bool PAIR = MX4 && std::is_same_v<T, _Float16>;  // tokens split into two bf16 values
+  constexpr int NA = 2 * RB;
   __shared__ float red[kUpWaves][NA][64][4];
   __shared__ int32_t token[kMaxTokens];
   const MoeSlot slot = p.slots[blockIdx.y];
   const int e = __builtin_amdgcn_readfirstlane(slot.expert);
   if (e < 0) return;
   const uint64_t mask = slot.mask;
-  const int n = __popcll(mask);
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
+  const int n = __builtin_amdgcn_readfirstlane(__popcll(mask));
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15;
   if (tid < 64 && (mask >> tid & 1)) token[__popcll(mask & ((1ull << tid) - 1))] = tid;
   __syncthreads();
   const int f0 = blockIdx.x * 16 * RB, rows = min(16 * RB, p.F - f0);
   const int64_t row0 = (int64_t)e * 2 * p.F + f0;
   constexpr int KU = MX4 ? 256 : 32;
   const int units = (p.D + KU - 1) / KU, k0 = units * wave / kUpWaves * KU, k1 = units * (wave + 1) / kUpWaves * KU;
-  const int64_t plane_h = (int64_t)p.T * p.top_k * p.F;
-  auto work = [&](auto ctc) {
-    constexpr int CT = decltype(ctc)::value;
+  const uint32_t x_row = (uint32_t)(MX4 ? panels_of(p.D) : p.D) * 2u;
+  const int64_t h_row = MX4 ? panels_of(p.F) : p.F;
+  // the tokens of rank base .. base + (16 or 8) CT - 1
+  auto work = [&](auto ctc, int base) {
+    constexpr int CT = decltype(ctc)::value, TOKENS = PAIR ? kPairTokens<CT> : 16 * CT, TILES = (TOKENS + 15) / 16;
     uint32_t col[CT];
 #pragma unroll
-    for (int c = 0; c < CT; ++c) col[c] = c * 16 + r < n ? (uint32_t)token[c * 16 + r] * (uint32_t)p.D * 2u : kOutOfRange;
+    for (int c = 0; c < CT; ++c) {
+      const int j = c * 16 + r, rank = base + j % TOKENS;
+      col[c] = rank >= n ? kOutOfRange
+               : PAIR    ? (uint32_t)(token[rank] * 2 + j / TOKENS) * x_row
+                         : (uint32_t)token[rank] * x_row;
+    }
     f32x4 acc[NA][CT] = {};
-    const uint32_t x_bytes = (uint32_t)p.T * (uint32_t)p.D * 2u;
+    const int rot = (int)(blockIdx.x >> 3) + 2 * wave;
     if constexpr (MX4) {
-      Stream4<2, RB, CT, PL> st;
+      Stream4<2, RB, CT> st;
       st.pitch = (uint32_t)p.D / 2u;
       st.panel = (int64_t)p.local * 2 * p.F * 8;
 #pragma unroll
@@ -479,28 +546,28 @@ __global__ __launch_bounds__(64 * kUpWaves, 2) void moe_up(MoeParams p) {
         st.scales[m] = p.gate_up_s + (row0 + m * p.F) * 8;
         st.rows[m] = rows;
       }
-      st.rc[0] = make_rsrc(SPLIT ? p.x_split : p.x, x_bytes);
-      if constexpr (SPLIT) st.rc[1] = make_rsrc(p.x_split + (int64_t)p.T * p.D, x_bytes);
-      st.run(k0, k1, p.D, col, acc);
+      st.rc = make_rsrc(p.x_panels, (uint32_t)p.T * x_row * (PAIR ? 2u : 1u));
+      st.run(k0, k1, p.D, rot, col, acc);
     } else {
-      Stream16<C, 2, RB, CT, PL> st;
-      st.pitch = (uint32_t)p.D * 2u;
+      Stream16<C, 2, RB, CT> st;
+      st.pitch = x_row;
 #pragma unroll
       for (int m = 0; m < 2; ++m) st.rw[m] = make_rsrc(p.gate_up + (row0 + m * p.F) * st.pitch, rows * st.pitch);
-      st.rc[0] = make_rsrc(p.x, x_bytes);
-      st.run(k0, k1, p.D, col, acc);
+      st.rc = make_rsrc(p.x, (uint32_t)p.T * x_row);
+      st.run(k0, k1, p.D, rot, col, acc);
     }
+    if constexpr (PAIR) fold(acc);
 #pragma unroll
-    for (int c = 0; c < CT; ++c) {
-      if (c) __syncthreads();
+    for (int c = 0; c < TILES; ++c) {
+      if (c || base) __syncthreads();
 #pragma unroll
       for (int i = 0; i < NA; ++i) *reinterpret_cast<f32x4 *>(red[wave][i][lane]) = acc[i][c];
       __syncthreads();
       // value (row block b, f, column): f fastest, so that neighbours write neighbours
       for (int i = tid; i < RB * 256; i += 64 * kUpWaves) {
         const int q = i & 3, gg = (i >> 2) & 3, b = (i >> 4) % RB, cc = i / (16 * RB), l = gg * 16 + cc;
-        const int column = c * 16 + cc, ff = f0 + b * 16 + gg * 4 + q;
-        if (column >= n || ff >= p.F) continue;
+        const int rank = base + c * 16 + cc, ff = f0 + b * 16 + gg * 4 + q;
+        if (c * 16 + cc >= TOKENS || rank >= n || ff >= p.F) continue;
         float a = 0, u = 0;
 #pragma unroll
         for (int w = 0; w < kUpWaves; ++w) {
@@ -508,26 +575,35 @@ __global__ __launch_bounds__(64 * kUpWaves, 2) void moe_up(MoeParams p) {
           u += red[w][RB + b][l][q];
         }
         const float v = a / (1.0f + __expf(-a)) * u;
-        const int64_t at = (int64_t)(slot.row + column) * p.F + ff;
+        C *h = reinterpret_cast<C *>(p.h) + (slot.row + rank) * 2 * h_row + (MX4 ? panel_place(ff) : ff);
         const C hi = (C)v;
-        const C lo = fabsf((float)hi) < __builtin_inff() ? (C)(v - (float)hi) : (C)0.0f;
-        reinterpret_cast<C *>(p.h)[at] = hi;
-        reinterpret_cast<C *>(p.h)[plane_h + at] = lo;
+        h[0] = hi;
+        h[h_row] = fabsf((float)hi) < __builtin_inff() ? (C)(v - (float)hi) : (C)0.0f;
       }
     }
   };
   using std::integral_constant;
-  if (CTMAX == 1 || n <= 16) work(integral_constant<int, 1>{});
-  else if constexpr (CTMAX > 1) {
-    if (CTMAX == 2 || n <= 32) work(integral_constant<int, 2>{});
-    else if constexpr (CTMAX > 2) work(integral_constant<int, 4>{});
+  constexpr int ONE = PAIR ? 8 : 16;  // tokens of one tile of columns
+  if (CTMAX == 1 || n <= ONE) {
+    work(integral_constant<int, 1>{}, 0);
+  } else if constexpr (CTMAX > 1) {
+    if (CTMAX == 2 || n <= 2 * ONE) {
+      work(integral_constant<int, 2>{}, 0);
+    } else if constexpr (CTMAX > 2) {
+      // past 4 tiles the weights are read again, now from cache
+      for (int base = 0; base < n; base += 4 * ONE) work(integral_constant<int, 4>{}, base);
+    }
   }
 }
 
 // Down: 16 RB outputs of every token per workgroup; the waves of `splits`
 // workgroups share the active experts' ffn evenly, an expert after the other.
+// h comes as pairs of 16-bit values, [row][2][F] (F in panels with 4-bit weights).
+// DENSE (at most 8 tokens): columns t and t + 8 are token t; otherwise an
+// expert's tokens are packed into as few tiles as hold them, and the results
+// moved to the tokens' places (TT tiles of 16 tokens).
 constexpr int kDownWaves = 8;
-template <typename T, bool MX4, int RB, int CTMAX>
+template <typename T, bool MX4, int RB, bool DENSE, int TT>
 __global__ __launch_bounds__(64 * kDownWaves, 2) void moe_down(MoeParams p) {
   using C = std::conditional_t<MX4, __bf16, T>;
   __shared__ float red[kDownWaves][RB][64][4];
@@ -538,61 +614,60 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void moe_down(MoeParams p) {
   const int64_t total = (int64_t)p.head[0] * units;
   const int part = blockIdx.y * kDownWaves + wave, parts = p.splits * kDownWaves;
   int64_t u = total * part / parts;
-  const int64_t u_end = total * (part + 1) / parts, plane = (int64_t)p.T * p.top_k * p.F;
-  const uint32_t h_bytes = (uint32_t)(plane * 2);
-  f32x4 sum[RB][CTMAX] = {};
+  const int64_t u_end = total * (part + 1) / parts;
+  const uint32_t h_row = (uint32_t)(MX4 ? panels_of(p.F) : p.F) * 2u;
+  f32x4 sum[RB][TT] = {};
   while (u < u_end) {
     const int at = (int)(u / units), first = (int)(u - (int64_t)at * units);
     const int last = (int)min((int64_t)units, first + (u_end - u));
     u += last - first;
     const MoeSlot slot = p.slots[at];
-    const int e = __builtin_amdgcn_readfirstlane(slot.expert), n = __popcll(slot.mask);
+    const int e = __builtin_amdgcn_readfirstlane(slot.expert), n = __builtin_amdgcn_readfirstlane(__popcll(slot.mask));
     const int64_t row0 = (int64_t)e * p.D + d0;
-    // CT tiles of columns; with CTMAX == 1 column r is token r, otherwise the
-    // expert's tokens from the one of rank `base` on are packed into the columns
     auto work = [&](auto ctc, int base) {
-      constexpr int CT = decltype(ctc)::value;
+      constexpr int CT = decltype(ctc)::value, TOKENS = kPairTokens<CT>;
       uint32_t col[CT];
 #pragma unroll
       for (int c = 0; c < CT; ++c) {
-        const int rank = CTMAX == 1 ? __popcll(slot.mask & ((1ull << r) - 1)) : base + c * 16 + r;
-        const bool has = CTMAX == 1 ? slot.mask >> r & 1 : rank < n;
-        col[c] = has ? (uint32_t)(slot.row + rank) * (uint32_t)p.F * 2u : kOutOfRange;
+        const int j = c * 16 + r, t = j % TOKENS;
+        const int rank = DENSE ? __popcll(slot.mask & ((1ull << t) - 1)) : base + t;
+        const bool has = DENSE ? (slot.mask >> t & 1) : rank < n;
+        col[c] = has ? (uint32_t)(rank * 2 + j / TOKENS) * h_row : kOutOfRange;
       }
       f32x4 acc[RB][CT] = {};
+      const uint16_t *h = p.h + (int64_t)slot.row * h_row;
       if constexpr (MX4) {
-        Stream4<1, RB, CT, 2> st;
+        Stream4<1, RB, CT> st;
         st.pitch = (uint32_t)p.F / 2u;
         st.panel = (int64_t)p.local * p.D * 8;
         st.rw[0] = make_rsrc(p.down + row0 * st.pitch, rows * st.pitch);
         st.scales[0] = p.down_s + row0 * 8;
         st.rows[0] = rows;
-        st.rc[0] = make_rsrc(p.h, h_bytes);
-        st.rc[1] = make_rsrc(p.h + plane, h_bytes);
-        st.run(first * KU, last * KU, p.F, col, acc);
+        st.rc = make_rsrc(h, (uint32_t)n * 2u * h_row);
+        st.run(first * KU, last * KU, p.F, 0, col, acc);
       } else {
-        Stream16<C, 1, RB, CT, 2> st;
+        Stream16<C, 1, RB, CT> st;
         st.pitch = (uint32_t)p.F * 2u;
         st.rw[0] = make_rsrc(p.down + row0 * st.pitch, rows * st.pitch);
-        st.rc[0] = make_rsrc(p.h, h_bytes);
-        st.rc[1] = make_rsrc(p.h + plane, h_bytes);
-        st.run(first * KU, last * KU, p.F, col, acc);
+        st.rc = make_rsrc(h, (uint32_t)n * 2u * h_row);
+        st.run(first * KU, last * KU, p.F, 0, col, acc);
       }
+      fold(acc);
       // only the expert's own tokens: a NaN or an infinity in its weights stays with them
 #pragma unroll
-      for (int c = 0; c < CTMAX; ++c) {
+      for (int c = 0; c < TT; ++c) {
         const int t = c * 16 + r, rank = __popcll(slot.mask & ((1ull << t) - 1)), pos = rank - base;
-        const bool mine = (slot.mask >> t & 1) && pos >= 0 && pos < CT * 16;
+        const bool mine = (slot.mask >> t & 1) && pos >= 0 && pos < TOKENS;
         const float w = mine ? p.row_w[slot.row + rank] : 0.0f;
 #pragma unroll
         for (int i = 0; i < RB; ++i)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             float v = acc[i][0][q];
-            if constexpr (CTMAX > 1) {
+            if constexpr (!DENSE) {
               const int from = (pos & 15) + g * 16;
               v = __shfl(acc[i][0][q], from);
-              if constexpr (CT > 1) {
+              if constexpr (CT > 2) {
                 const float o = __shfl(acc[i][1][q], from);
                 v = pos >= 16 ? o : v;
               }
@@ -602,15 +677,19 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void moe_down(MoeParams p) {
       }
     };
     using std::integral_constant;
-    if (CTMAX == 1 || n <= 16) {
+    if (DENSE || n <= 8) {
       work(integral_constant<int, 1>{}, 0);
-    } else if constexpr (CTMAX > 1) {
-      // past 32 tokens of one expert its rows are read again, now from cache
-      for (int base = 0; base < n; base += 32) work(integral_constant<int, 2>{}, base);
+    } else if constexpr (!DENSE) {
+      if (TT == 1 || n <= 16) {
+        work(integral_constant<int, 2>{}, 0);
+      } else if constexpr (TT > 1) {
+        // past 32 tokens of one expert its rows are read again, now from cache
+        for (int base = 0; base < n; base += 32) work(integral_constant<int, 4>{}, base);
+      }
     }
   }
 #pragma unroll
-  for (int c = 0; c < CTMAX; ++c) {
+  for (int c = 0; c < TT; ++c) {
     if (c) __syncthreads();
 #pragma unroll
     for (int i = 0; i < RB; ++i) *reinterpret_cast<f32x4 *>(red[wave][i][lane]) = sum[i][c];
@@ -640,31 +719,33 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void moe_down(MoeParams p) {
   }
 }
 
-template <typename T, bool MX4, int RBU, int RBD, int CT>
+template <typename T, bool MX4, int RBU, int CTU, int RBD, bool DENSE, int TT>
 int launch_sized(MoeParams p, int cus, hipStream_t s) {
-  constexpr bool SPLIT = MX4 && std::is_same_v<T, _Float16>;
-  const int split = SPLIT ? (int)(((int64_t)p.T * p.D + 64 * kRouterWaves * 4 - 1) / (64 * kRouterWaves * 4)) : 0;
-  moe_router<T><<<p.expert_wgs * p.tiles + split, 64 * kRouterWaves, 0, s>>>(p);
+  // workgroups that lay the tokens out: 8 values a thread
+  const int lay = MX4 ? (p.T * (p.D / 8) + 64 * kRouterWaves - 1) / (64 * kRouterWaves) : 0;
+  moe_router<T><<<p.expert_wgs * p.tiles + lay, 64 * kRouterWaves, 0, s>>>(p);
   if (hipGetLastError() != hipSuccess) return FO_ERR_HIP;
-  moe_up<T, MX4, RBU, CT><<<dim3((p.F + 16 * RBU - 1) / (16 * RBU), p.most), 64 * kUpWaves, 0, s>>>(p);
+  moe_up<T, MX4, RBU, CTU><<<dim3((p.F + 16 * RBU - 1) / (16 * RBU), p.most), 64 * kUpWaves, 0, s>>>(p);
   if (hipGetLastError() != hipSuccess) return FO_ERR_HIP;
-  // enough workgroups for two a CU, as long as every wave has a few steps of K
+  // a workgroup for every CU, as long as every wave has a few steps of K
   const int tiles = (p.D + 16 * RBD - 1) / (16 * RBD), units = (p.F + 255) / 256;
-  int splits = (2 * cus + tiles - 1) / tiles;
+  int splits = (cus + tiles - 1) / tiles;
   const int64_t most = (int64_t)p.most * units / (kDownWaves * 2);
   if (splits > most) splits = (int)most;
   if (splits > kMoeMaxSplits) splits = kMoeMaxSplits;
   p.splits = splits < 1 ? 1 : splits;
-  moe_down<T, MX4, RBD, CT><<<dim3(tiles, p.splits), 64 * kDownWaves, 0, s>>>(p);
+  moe_down<T, MX4, RBD, DENSE, TT><<<dim3(tiles, p.splits), 64 * kDownWaves, 0, s>>>(p);
   return hipGetLastError() == hipSuccess ? FO_OK : FO_ERR_HIP;
 }
 
 template <typename T, bool MX4>
 int launch_typed(const MoeParams &p, int cus, hipStream_t s) {
-  if (p.T <= 4) return launch_sized<T, MX4, 1, 1, 1>(p, cus, s);
-  if (p.T <= 16) return launch_sized<T, MX4, 2, 4, 1>(p, cus, s);
-  if (p.T <= 32) return launch_sized<T, MX4, 2, 4, 2>(p, cus, s);
-  return launch_sized<T, MX4, 2, 4, 4>(p, cus, s);
+  constexpr int X = MX4 && std::is_same_v<T, _Float16> ? 2 : 1;  // columns of a token in the first product
+  if (p.T <= 4) return launch_sized<T, MX4, 1, 1, 1, true, 1>(p, cus, s);
+  if (p.T <= 8) return launch_sized<T, MX4, 2, 1, 2, true, 1>(p, cus, s);
+  if (p.T <= 16) return launch_sized<T, MX4, 2, X, 2, false, 1>(p, cus, s);
+  if (p.T <= 32) return launch_sized<T, MX4, 2, 2 * X, 2, false, 2>(p, cus, s);
+  return launch_sized<T, MX4, 2, 4, 2, false, 4>(p, cus, s);
 }
 
 }  // namespace
@@ -691,7 +772,7 @@ int launch_moe(const fo_moe_desc &d, int32_t tokens, const void *x, const void *
   p.ids = reinterpret_cast<int32_t *>(ws + l.ids);
   p.wts = reinterpret_cast<float *>(ws + l.wts);
   p.logits = reinterpret_cast<float *>(ws + l.logits);
-  p.x_split = reinterpret_cast<uint16_t *>(ws + l.x_split);
+  p.x_panels = reinterpret_cast<uint16_t *>(ws + l.x_panels);
   p.h = reinterpret_cast<uint16_t *>(ws + l.h);
   p.partial = reinterpret_cast<float *>(ws + l.partial);
   p.T = tokens;

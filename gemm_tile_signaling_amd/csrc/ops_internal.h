@@ -29,8 +29,8 @@ struct MoeLayout {
   int64_t ids;       // int32 [max_tokens][top_k]: picked experts
   int64_t wts;       // float [max_tokens][top_k]: their weights
   int64_t logits;    // float [max_tokens][experts]
-  int64_t x_split;   // bf16 [2][max_tokens][hidden]: fp16 tokens as two bf16 values (4-bit weights only)
-  int64_t h;         // 16-bit [2][max_tokens * top_k][ffn]: the activations as pairs
+  int64_t x_panels;  // bf16 [max_tokens][1, or 2 for fp16][hidden, whole panels]: the tokens (4-bit weights only)
+  int64_t h;         // 16-bit [max_tokens * top_k][2][ffn, whole panels with 4-bit weights]: the activations as pairs
   int64_t partial;   // float [kMoeMaxSplits][max_tokens][hidden]
   int64_t bytes;
 };
@@ -42,6 +42,8 @@ inline MoeLayout moe_layout(const fo_moe_desc &d) {
     at += (bytes + 255) / 256 * 256;
     return here;
   };
+  const bool mx4 = d.weights == FO_MOE_MX4;
+  auto whole = [](int64_t k) { return (k + 255) / 256 * 256; };
   const int64_t picks = (int64_t)d.max_tokens * d.top_k;
   l.counters = take(4 * (8 + (d.hidden + 15) / 16));
   l.head = take(4);
@@ -50,8 +52,8 @@ inline MoeLayout moe_layout(const fo_moe_desc &d) {
   l.ids = take(4 * picks);
   l.wts = take(4 * picks);
   l.logits = take(4 * (int64_t)d.max_tokens * d.experts);
-  l.x_split = take(d.weights == FO_MOE_MX4 && d.dtype == FO_FP16 ? 4 * d.max_tokens * d.hidden : 0);
-  l.h = take(4 * picks * d.ffn);
+  l.x_panels = take(mx4 ? 2 * (d.dtype == FO_FP16 ? 2 : 1) * d.max_tokens * whole(d.hidden) : 0);
+  l.h = take(4 * picks * (mx4 ? whole(d.ffn) : d.ffn));
   l.partial = take(4 * (int64_t)kMoeMaxSplits * d.max_tokens * d.hidden);
   l.bytes = at;
   return l;

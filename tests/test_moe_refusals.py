@@ -35,8 +35,8 @@ def test_description(change, code):
 def test_workspace_size():
     rc, n = _bytes()
     assert rc == 0 and n % 256 == 0 and n >= 4 * 4 * 2 * 96
-    # 4-bit weights with fp16 tokens keep the tokens as two bf16 values as well
-    assert _bytes(weights=1, dtype=1)[1] == _bytes(weights=1, dtype=0)[1] + 4 * 4 * 64
+    # 4-bit weights: the tokens laid out in panels of 256 values, fp16 ones as two bf16 values
+    assert _bytes(weights=1, dtype=1)[1] == _bytes(weights=1, dtype=0)[1] + 2 * 4 * 256
     assert moe._ops().fo_moe_workspace_bytes(None, None) == INVALID
     layer = fo.Moe(64, 96, 8, 2, first_expert=2, max_tokens=4)
     assert layer.local_experts == 6
