@@ -366,26 +366,39 @@ struct Stream16 {
       }
     }
   }
+  __device__ __forceinline__ void load_x(u32x4 (&x)[U][CT], int k, int end, int g, const uint32_t (&col)[CT]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int kk = k + u * 32 + g * 8;
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+        x[u][c] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                rc, kk < end && col[c] < kOutOfRange ? col[c] + kk * 2u : kOutOfRange, 0, 0));
+    }
+  }
+  // A group's weights and columns are loaded while the group before is multiplied.
   __device__ __forceinline__ void run(int k0, int k1, int K, int rot, const uint32_t (&col)[CT], f32x4 (&acc)[NA][CT]) {
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, end = min(k1, K);
     if (k0 >= end) return;
     const int groups = (end - k0 + U * 32 - 1) / (U * 32);
     int group = rot % groups;
+    u32x4 next[U][CT];
+    load_x(next, k0 + group * U * 32, end, g, col);
     load_a(k0 + group * U * 32, end, r, g);
     for (int n = 0; n < groups; ++n) {
       u32x4 x[U][CT], w[U][NA];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int kk = k0 + (group * U + u) * 32 + g * 8;
 #pragma unroll
-        for (int c = 0; c < CT; ++c)
-          x[u][c] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                  rc, kk < end && col[c] < kOutOfRange ? col[c] + kk * 2u : kOutOfRange, 0, 0));
+        for (int c = 0; c < CT; ++c) x[u][c] = next[u][c];
 #pragma unroll
         for (int i = 0; i < NA; ++i) w[u][i] = a[u][i];
       }
       if (++group == groups) group = 0;
-      if (n + 1 < groups) load_a(k0 + group * U * 32, end, r, g);
+      if (n + 1 < groups) {
+        load_x(next, k0 + group * U * 32, end, g, col);
+        load_a(k0 + group * U * 32, end, r, g);
+      }
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -444,21 +457,35 @@ struct Stream4 {
         for (int c = 0; c < CT; ++c) acc[i][c] = mma16<__bf16>(v, x[j][c], acc[i][c]);
       }
   }
-  // Loads return in order, so the columns of a panel (from cache) are asked for
-  // before the next panel's weights (from memory): waiting for them then does
-  // not wait for the weights.
+  // With one tile of columns a panel's weights and columns are loaded while the
+  // panel before is multiplied; with more there are no registers for that, and
+  // the columns (from cache) are asked for before the next panel's weights (from
+  // memory): loads return in order, so waiting for them does not wait for those.
   __device__ __forceinline__ void run(int k0, int k1, int K, int rot, const uint32_t (&col)[CT], f32x4 (&acc)[NA][CT]) {
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, end = min(k1, K), nb = end / 32;
     if (k0 >= end) return;
     const int groups = (end - k0 + 255) / 256;
     int group = rot % groups;
+    u32x4 n0[4][CT], n1[4][CT];
+    if constexpr (CT == 1) {
+      load_x(n0, k0 + group * 256, 0, end, g, col);
+      load_x(n1, k0 + group * 256, 1, end, g, col);
+    }
     load_a(k0 + group * 256, end, r, g);
     for (int n = 0; n < groups; ++n) {
       u32x4 w0[NA], w1[NA], x0[4][CT], x1[4][CT];
       float f0[NA], f1[NA];
       const int k = k0 + group * 256, b = k / 32 + g * 2;
-      load_x(x0, k, 0, end, g, col);
-      if constexpr (CT <= 2) load_x(x1, k, 1, end, g, col);
+      if constexpr (CT == 1) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x0[j][0] = n0[j][0];
+          x1[j][0] = n1[j][0];
+        }
+      } else {
+        load_x(x0, k, 0, end, g, col);
+        if constexpr (CT == 2) load_x(x1, k, 1, end, g, col);
+      }
 #pragma unroll
       for (int i = 0; i < NA; ++i) {
         w0[i] = a[i][0];
@@ -472,7 +499,13 @@ struct Stream4 {
         load_x(x1, k, 1, end, g, col);
       }
       if (++group == groups) group = 0;
-      if (n + 1 < groups) load_a(k0 + group * 256, end, r, g);
+      if (n + 1 < groups) {
+        if constexpr (CT == 1) {
+          load_x(n0, k0 + group * 256, 0, end, g, col);
+          load_x(n1, k0 + group * 256, 1, end, g, col);
+        }
+        load_a(k0 + group * 256, end, r, g);
+      }
       if constexpr (CT <= 2) multiply(w0, f0, x0, acc);
       multiply(w1, f1, x1, acc);
     }

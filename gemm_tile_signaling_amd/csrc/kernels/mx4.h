@@ -15,6 +15,7 @@ typedef __attribute__((ext_vector_type(16))) float f32x16;
 typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
 typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4;
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+typedef __attribute__((ext_vector_type(2))) _Float16 f16x2;
 typedef __attribute__((ext_vector_type(4))) _Float16 f16x4;
 typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
 
@@ -29,11 +30,6 @@ __device__ __forceinline__ uint32_t mx4_scale_byte(uint32_t top) {
 // field alone, 255 as NaN; byte 0 is 2^-127, a denormal in fp32).
 __device__ __forceinline__ float mx4_scale(uint32_t byte) {
   return __uint_as_float(byte == 0 ? 0x00400000u : byte << 23);
-}
-
-// lo / scale and hi / scale as one byte of two codes.
-__device__ __forceinline__ uint32_t mx4_pair(float lo, float hi, float scale) {
-  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, lo, hi, scale, 0) & 0xFFu;
 }
 
 template <typename T>

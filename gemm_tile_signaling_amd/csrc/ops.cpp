@@ -52,9 +52,8 @@ int fo_mx4_quantize(const void *x, int64_t rows, int64_t cols, int64_t ld, int32
   if (rows == 0) return FO_OK;
   if (!aligned(x, 2) || !aligned(codes, 16) || !aligned(scales, 16)) return FO_ERR_INVALID;
   if (rows > (1ll << 40) || ld > (1ll << 40) / rows) return FO_ERR_UNSUPPORTED;
-  const int cus = device_cus();
-  if (cus < 0) return cus;
-  return fo::launch_mx4_quantize(x, rows, cols, ld, dtype, codes, scales, cus, stream);
+  if (const int cus = device_cus(); cus < 0) return cus;
+  return fo::launch_mx4_quantize(x, rows, cols, ld, dtype, codes, scales, stream);
 }
 
 int fo_mx4_dequantize(const void *codes, const void *scales, int64_t rows, int64_t cols, int32_t out_type, void *out,
@@ -63,9 +62,8 @@ int fo_mx4_dequantize(const void *codes, const void *scales, int64_t rows, int64
   if (rows == 0) return FO_OK;
   if (!aligned(codes, 16) || !aligned(scales, 16) || !aligned(out, out_type == FO_FP32 ? 4 : 2)) return FO_ERR_INVALID;
   if (rows > (1ll << 40) || cols > (1ll << 40) / rows) return FO_ERR_UNSUPPORTED;
-  const int cus = device_cus();
-  if (cus < 0) return cus;
-  return fo::launch_mx4_dequantize(codes, scales, rows, cols, out_type, out, cus, stream);
+  if (const int cus = device_cus(); cus < 0) return cus;
+  return fo::launch_mx4_dequantize(codes, scales, rows, cols, out_type, out, stream);
 }
 
 int fo_mx4_gemm(const void *a_codes, const void *a_scales, const void *b_codes, const void *b_scales, void *out,

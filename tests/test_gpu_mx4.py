@@ -85,6 +85,21 @@ def test_quantize_strided_rows(rows, cols, ld, at, dtype):
         assert np.array_equal(got[0].cpu().numpy(), want[0]) and np.array_equal(got[1].cpu().numpy(), want[1])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_large_matrices_are_quantised_like_their_parts(dtype):
+    """Past 32 MB of 16-bit values the memory accesses differ; the bits must not."""
+    rows, cols = 4111, 4131
+    wide = (torch.randn(rows, cols + 3, device="cuda") * 5).to(TORCH[dtype])
+    wide[17, 100] = float("inf")
+    x = wide[:, :cols]
+    codes, scales = fo.mx4_quantize(x)
+    back = fo.mx4_dequantize(codes, scales, cols, dtype=dtype)
+    for a in range(0, rows, 1000):
+        c, s = fo.mx4_quantize(x[a:a + 1000])
+        assert torch.equal(codes[a:a + 1000], c) and torch.equal(scales[:, a:a + 1000], s)
+        assert torch.equal(back[a:a + 1000].view(torch.int16), fo.mx4_dequantize(c, s, cols, dtype=dtype).view(torch.int16))
+
+
 def random_form(seed, rows, k, lo=0, hi=256):
     rng = np.random.default_rng(seed)
     return rng.integers(0, 16, (rows, k)).astype(np.uint8), rng.integers(lo, hi, (rows, k // 32)).astype(np.uint8)
