@@ -94,7 +94,7 @@ constexpr uint32_t kOutOfRange = 0xC0000000u;  // a byte offset past every buffe
 // a ring of NS LDS stages; NW waves in a WGM x WGN grid.
 template <int BM, int BN, int NW, int NS_>
 struct Cfg {
-  static constexpr int THREADS = 64 * NW, NS = NS_, DIST = NS - 1;
+  static constexpr int THREADS = 64 * NW, NS = NS_;
   static constexpr int WGM = 2, WGN = NW / 2;
   static constexpr int WM = BM / WGM, WN = BN / WGN, FM = WM / 32, FN = WN / 32;
   static constexpr int ROWB = 128, CHUNKS = 8, KS = 4;   // a slice is 4 k-steps of 64 values
@@ -102,13 +102,16 @@ struct Cfg {
   // scale bytes of a slice: 8 a row, loaded 4 a lane: 2 BM + 2 BN lanes
   static constexpr int S_PER_T = (2 * BM + 2 * BN) / THREADS;
   static constexpr int LOADS = A_PER_T + B_PER_T + S_PER_T;
-  static constexpr int DPB = NS == 2 ? LOADS : (LOADS + KS - 1) / KS;  // loads issued per k-step
+  // Of a slice's loads, those issued beside the last k-step of the slice that frees its
+  // stage; the rest follow a k-step later (all of them at once hold the wave up: 2 - 7%
+  // slower on 256 x 256 tiles).
+  static constexpr int EARLY = LOADS / 3;
   static constexpr int B_AT = BM * ROWB, S_AT = (BM + BN) * ROWB, STAGE = S_AT + (BM + BN) * 8;
   static constexpr int OUT_PITCH = 80;                   // a wave's 32 x 32 block: 64 bytes a row, padded
   static constexpr int OUT_AT = NS * STAGE, LDS = OUT_AT + NW * 32 * OUT_PITCH;
   static constexpr int STORES = FM * FN * 2;
   static_assert(BM * CHUNKS % THREADS == 0 && BN * CHUNKS % THREADS == 0 && (S_PER_T == 1 || (S_PER_T == 2 && BM == BN)), "chunk split");
-  static_assert(DIST * LOADS + STORES <= 63, "operations in flight fit the vmcnt counter");
+  static_assert(NS * LOADS + STORES <= 63, "operations in flight fit the vmcnt counter");
   static_assert(LDS <= 160 * 1024, "LDS of one CU");
 };
 
@@ -194,16 +197,12 @@ __global__ __launch_bounds__(64 * NW, 2) void mx4_gemm_tiled(Mx4Params p) {
     });
   };
   using std::integral_constant;
-  auto dma_part = [&](auto partc, int kt) {
-    constexpr int part = decltype(partc)::value;
-    constexpr int q0 = part * C::DPB < C::LOADS ? part * C::DPB : C::LOADS;
-    constexpr int q1 = q0 + C::DPB < C::LOADS ? q0 + C::DPB : C::LOADS;
-    dma(integral_constant<int, q0>{}, integral_constant<int, q1>{}, kt);
-  };
-  auto prologue = [&]() {  // slices 0 .. NS-2
+  // Slices 0 .. NS-2, and the part of slice NS-1 that a last k-step would have issued
+  auto prologue = [&]() {
 #pragma unroll
-    for (int kt = 0; kt < C::DIST; ++kt)
+    for (int kt = 0; kt < C::NS - 1; ++kt)
       if (kt < nk) dma(integral_constant<int, 0>{}, integral_constant<int, C::LOADS>{}, kt);
+    if (C::NS - 1 < nk) dma(integral_constant<int, 0>{}, integral_constant<int, C::EARLY>{}, C::NS - 1);
   };
 
   const int64_t step = gridDim.x;
@@ -247,65 +246,69 @@ __global__ __launch_bounds__(64 * NW, 2) void mx4_gemm_tiled(Mx4Params p) {
       constexpr int ND = decltype(ndc)::value, R = decltype(nrc)::value;
       static_for<0, R>([&](auto rc_) {
         constexpr int r = decltype(rc_)::value;
-        if constexpr (r % 2 == 0 && r / 2 < ND) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // VMEM read
+        if constexpr (r < ND) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);                        // VMEM read
         __builtin_amdgcn_sched_group_barrier(0x100, R > NM ? 2 : 1, 0);                               // DS read
         if constexpr (r < NM) __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                     // MFMA
       });
-      if constexpr ((R + 1) / 2 < ND) __builtin_amdgcn_sched_group_barrier(0x020, ND - (R + 1) / 2, 0);
+      if constexpr (R < ND) __builtin_amdgcn_sched_group_barrier(0x020, ND - R, 0);
       if constexpr (NM > R) __builtin_amdgcn_sched_group_barrier(0x008, NM - R, 0);
       __builtin_amdgcn_sched_barrier(0);
     };
     // k-steps 0 .. 2 of a slice, each reading the next step's fragments, with the slice's share of loads
     auto blocks = [&](int kt, auto dmac) {
+      constexpr bool DMA = decltype(dmac)::value;  // the rest of slice kt + NS - 1
       __builtin_amdgcn_sched_barrier(0);
       static_for<0, 3>([&](auto sc) {
         constexpr int st = decltype(sc)::value;
-        if constexpr (decltype(dmac)::value) dma_part(sc, kt + C::DIST);
+        if constexpr (DMA && st == 0) dma(integral_constant<int, C::EARLY>{}, integral_constant<int, C::LOADS>{}, kt + C::NS - 1);
         read_frags(integral_constant<int, (st + 1) % 2>{}, kt, st + 1);
         mfmas(integral_constant<int, st % 2>{}, sc);
-        constexpr int left_q = C::LOADS - st * C::DPB;
-        order(integral_constant<int, decltype(dmac)::value ? (left_q < 0 ? 0 : left_q < C::DPB ? left_q : C::DPB) : 0>{},
-              integral_constant<int, NR>{});
+        order(integral_constant<int, DMA && st == 0 ? C::LOADS - C::EARLY : 0>{}, integral_constant<int, NR>{});
       });
     };
     // the last k-step, beside the first reads of the next slice (which has landed for every wave)
-    auto hand_over = [&](int kt) {
+    auto hand_over = [&](int kt, auto dmac) {
       uint32_t ta[C::FM], tb[C::FN];
+      constexpr bool DMA = decltype(dmac)::value;
+      if constexpr (DMA) dma(integral_constant<int, 0>{}, integral_constant<int, C::EARLY>{}, kt + C::NS);
       read_scales(kt + 1, ta, tb);
       read_frags(integral_constant<int, 0>{}, kt + 1, 0);
       mfmas(integral_constant<int, 1>{}, integral_constant<int, 3>{});
-      order(integral_constant<int, 0>{}, integral_constant<int, 2 * NR>{});
+      order(integral_constant<int, DMA ? C::EARLY : 0>{}, integral_constant<int, 2 * NR>{});
 #pragma unroll
       for (int f = 0; f < C::FM; ++f) sa[f] = ta[f];
 #pragma unroll
       for (int f = 0; f < C::FN; ++f) sb[f] = tb[f];
     };
-    // slice 0 has landed once at most min(DIST - 1, nk - 1) slices, and the last tile's stores, are in flight
-    if (first)
-      wait_slices<C::LOADS, C::DIST - 1>(nk - 1);
+    // slice 0 has landed once the slices after it, as far as they are issued, and the last tile's stores are in flight
+    if (nk >= C::NS)
+      first ? __builtin_amdgcn_s_waitcnt(vmcnt_imm((C::NS - 2) * C::LOADS + C::EARLY))
+            : __builtin_amdgcn_s_waitcnt(vmcnt_imm((C::NS - 2) * C::LOADS + C::EARLY + C::STORES));
     else
-      wait_slices<C::LOADS, C::DIST - 1, C::STORES>(nk - 1);
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
     first = false;
     bare_barrier();
     read_scales(0, sa, sb);
     read_frags(integral_constant<int, 0>{}, 0, 0);
     int kt = 0;
-    for (; kt + C::DIST < nk; ++kt) {
+    for (; kt + C::NS < nk; ++kt) {
       blocks(kt, std::true_type{});
-      dma_part(integral_constant<int, 3>{}, kt + C::DIST);
       __builtin_amdgcn_s_waitcnt(kLgkmcntZero);  // this wave's reads of slice kt are complete
-      __builtin_amdgcn_s_waitcnt(vmcnt_imm((C::DIST - 1) * C::LOADS));
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm((C::NS - 2) * C::LOADS));  // slice kt + 1 has landed
       bare_barrier();
-      hand_over(kt);
+      hand_over(kt, std::true_type{});
     }
-    if constexpr (C::DIST > 1)
-      for (; kt + 1 < nk; ++kt) {
-        blocks(kt, std::false_type{});
-        __builtin_amdgcn_s_waitcnt(kLgkmcntZero);
-        wait_slices<C::LOADS, C::DIST - 2>(nk - 2 - kt);
-        bare_barrier();
-        hand_over(kt);
-      }
+    auto drain = [&](auto dmac) {
+      blocks(kt, dmac);
+      __builtin_amdgcn_s_waitcnt(kLgkmcntZero);
+      wait_slices<C::LOADS, C::NS - 2>(nk - 2 - kt);
+      bare_barrier();
+      hand_over(kt, std::false_type{});
+      ++kt;
+    };
+    if (kt + C::NS == nk) drain(std::true_type{});
+    if constexpr (C::NS > 2)
+      while (kt + 1 < nk) drain(std::false_type{});
     blocks(nk - 1, std::false_type{});
     mfmas(integral_constant<int, 1>{}, integral_constant<int, 3>{});
     __builtin_amdgcn_sched_barrier(0);
