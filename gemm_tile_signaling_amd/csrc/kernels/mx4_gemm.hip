@@ -370,11 +370,147 @@ int launch_tiled(Mx4Params p, int cus, hipStream_t s) {
   return hipGetLastError() == hipSuccess ? FO_OK : FO_ERR_HIP;
 }
 
+// Few rows of A (at most 16 CT): B is read once and little else happens, so it
+// goes from memory straight to registers, without LDS stages or barriers.  B's
+// rows are the MFMA's first operand (RB blocks of 16), A's rows its columns; the
+// waves of a workgroup each take a contiguous share of the panels (256 values)
+// and add their sums up through LDS.  A group of U panels is loaded while the
+// group before it is multiplied.  Bound: HBM.
+template <typename T, int RB, int CT, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void mx4_gemm_few(Mx4Params p) {
+  constexpr int U = RB * CT <= 2 ? 2 : 1;
+  __shared__ float red[NW][RB * CT][64][4];
+  const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t col_tile = blockIdx.x % (uint32_t)p.col_tiles;
+  int problem;
+  int64_t row0, row_end;
+  if (!find_rows(p, 16 * CT, blockIdx.x / (uint32_t)p.col_tiles, &problem, &row0, &row_end)) return;
+  const int64_t n0 = col_tile * 16 * RB, b_row0 = (int64_t)problem * p.N + n0;
+  const uint32_t rows = (uint32_t)min((int64_t)16 * CT, row_end - row0), cols = (uint32_t)min((int64_t)16 * RB, p.N - n0);
+  const uint32_t pitch = (uint32_t)p.nb * 16u;
+  const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.a + row0 * pitch, rows * pitch), rb = make_rsrc(p.b + b_row0 * pitch, cols * pitch);
+  const uint8_t *sa0 = p.as + row0 * 8, *sb0 = p.bs + b_row0 * 8;
+  const int64_t sa_panel = p.M * 8, sb_panel = (int64_t)p.problems * p.N * 8;
+  const int panels = (p.nb + 7) / 8, first = panels * wave / NW, last = panels * (wave + 1) / NW;
+
+  // Lane group g takes blocks 2 g and 2 g + 1 of a panel: 32 neighbouring bytes of codes, 2 of scales.
+  u32x4 b[U][RB][2], a[U][CT][2];
+  uint32_t sb[U][RB], sa[U][CT];
+  auto load = [&](int at) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int panel = at + u, block = panel * 8 + g * 2, left = panel < last ? p.nb - block : 0;
+      const __amdgpu_buffer_rsrc_t rsa = make_rsrc(sa0 + panel * sa_panel, panel < last ? rows * 8 : 0);
+      const __amdgpu_buffer_rsrc_t rsb = make_rsrc(sb0 + panel * sb_panel, panel < last ? cols * 8 : 0);
+#pragma unroll
+      for (int i = 0; i < RB; ++i) {
+        const uint32_t row = (uint32_t)(i * 16 + r);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          b[u][i][h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                     rb, h < left ? row * pitch + (block + h) * 16u : kOutOfRange, 0, 0));
+        sb[u][i] = __builtin_amdgcn_raw_buffer_load_b16(rsb, row * 8u + g * 2u, 0, 0);
+      }
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        const uint32_t row = (uint32_t)(c * 16 + r);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          a[u][c][h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                     ra, h < left ? row * pitch + (block + h) * 16u : kOutOfRange, 0, 0));
+        sa[u][c] = __builtin_amdgcn_raw_buffer_load_b16(rsa, row * 8u + g * 2u, 0, 0);
+      }
+    }
+  };
+  f32x4 acc[RB][CT] = {};
+  if (first < last) load(first);
+  for (int at = first; at < last; at += U) {
+    u32x4 bb[U][RB][2], aa[U][CT][2];
+    uint32_t sbb[U][RB], saa[U][CT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      // a byte past the row's last block says nothing: its codes are zeros, its scale must not be a NaN
+      const int left = p.nb - (at + u) * 8 - g * 2;
+      const uint32_t mask = left >= 2 ? 0xFFFFu : left == 1 ? 0xFFu : 0u;
+#pragma unroll
+      for (int i = 0; i < RB; ++i) {
+        bb[u][i][0] = b[u][i][0];
+        bb[u][i][1] = b[u][i][1];
+        sbb[u][i] = sb[u][i] & mask;
+      }
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        aa[u][c][0] = a[u][c][0];
+        aa[u][c][1] = a[u][c][1];
+        saa[u][c] = sa[u][c] & mask;
+      }
+    }
+    if (at + U < last) load(at + U);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < RB; ++i)
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          acc[i][c] = mx4_mma16<0, 0>(bb[u][i][0], sbb[u][i], aa[u][c][0], saa[u][c], acc[i][c]);
+          acc[i][c] = mx4_mma16<1, 1>(bb[u][i][1], sbb[u][i], aa[u][c][1], saa[u][c], acc[i][c]);
+        }
+  }
+#pragma unroll
+  for (int i = 0; i < RB; ++i)
+#pragma unroll
+    for (int c = 0; c < CT; ++c) *reinterpret_cast<f32x4 *>(red[wave][i * CT + c][lane]) = acc[i][c];
+  __syncthreads();
+  // four neighbouring outputs of a row a thread; outputs fastest
+  for (int q = tid; q < RB * CT * 64; q += 64 * NW) {
+    const int gg = q & 3, i = (q >> 2) % RB, m = q / (4 * RB), c = m / 16, l = gg * 16 + m % 16;
+    const int64_t n = n0 + i * 16 + gg * 4;
+    if (m >= (int)rows || n >= p.N) continue;
+    f32x4 v = {};
+#pragma unroll
+    for (int w = 0; w < NW; ++w) v += *reinterpret_cast<const f32x4 *>(red[w][i * CT + c][l]);
+    *reinterpret_cast<u32x2 *>(p.out + (row0 + m) * p.N + n) = pack4<T>(v);
+  }
+}
+
+template <typename T, int RB, int CT, int NW>
+int launch_few(Mx4Params p, hipStream_t s) {
+  // every problem with rows is one row tile
+  const int64_t row_tiles = p.row_ends ? (p.problems < p.M ? p.problems : p.M) : 1;
+  p.col_tiles = (int32_t)((p.N + 16 * RB - 1) / (16 * RB));
+  mx4_gemm_few<T, RB, CT, NW><<<dim3((uint32_t)(row_tiles * p.col_tiles)), 64 * NW, 0, s>>>(p);
+  return hipGetLastError() == hipSuccess ? FO_OK : FO_ERR_HIP;
+}
+
 template <typename T>
 int launch_any(const Mx4Params &p, int cus, hipStream_t s) {
-  auto tiles = [&](int64_t bm, int64_t bn) { return ((p.M + bm - 1) / bm + (p.problems - 1) / 2) * ((p.N + bn - 1) / bn); };
-  if (tiles(256, 256) >= cus) return launch_tiled<T, 256, 256, 8, 2>(p, cus, s);
-  if (tiles(128, 128) >= cus) return launch_tiled<T, 128, 128, 4, 2>(p, cus, s);
+  // Few rows.  With up to 32 the streaming kernel is ahead as long as a workgroup
+  // a CU covers B (16 x 8192 x 3584: 6.2 us, 64 x 64 tiles 7.9; 64 rows: 9.5 against
+  // 8.5); past that its re-reading of A costs more than the tiles' barriers, except
+  // for a handful of rows (14336 x 8192: one row 15.0 against 15.2 us, 16 rows 17.2
+  // against 15.6).  32 rows of B a workgroup, 16 where that leaves CUs idle or the
+  // chip is full anyway.
+  const int64_t one_a_cu = 32 * (int64_t)cus;
+  if (p.M <= 4 && p.N > one_a_cu + one_a_cu / 4) return launch_few<T, 1, 1, 4>(p, s);
+  if (p.M <= 32 && p.N <= one_a_cu + one_a_cu / 4) {
+    const bool wide = p.N >= one_a_cu;
+    if (p.M <= 16) return wide ? launch_few<T, 2, 1, 8>(p, s) : launch_few<T, 1, 1, 8>(p, s);
+    return wide ? launch_few<T, 2, 2, 8>(p, s) : launch_few<T, 1, 2, 8>(p, s);
+  }
+  // Otherwise the tile with the least time: rounds of tiles over the CUs, at the
+  // microseconds a slice that each tile was measured to take with one (c1) and two
+  // (c2) workgroups on a CU: 0.40 and 0.57 for 64 x 64, 0.92 and 1.44 for 128 x 128,
+  // 2.15 for 256 x 256, of which one fits.  (777 x 4104 x 2752: 18.5, 14.1 and 23.9 us;
+  // 512 x 4096 x 4096: 11.9, 17.9, 28.8; 1024 x 8192 x 8192: 77, 48, 62; 2048 rows: 159, 88, 68.)
+  auto time = [&](int64_t bm, double c1, double c2, int slots) {
+    const int64_t tiles = ((p.M + bm - 1) / bm + (p.problems - 1) / 2) * ((p.N + bm - 1) / bm);
+    const int64_t full = tiles / (slots * cus), left = tiles % (slots * cus);
+    return full * c2 + (left == 0 ? 0.0 : left <= cus ? c1 : c2);
+  };
+  const double t64 = time(64, 0.40, 0.57, 2), t128 = time(128, 0.92, 1.44, 2), t256 = time(256, 2.15, 2.15, 1);
+  if (t256 <= t128 && t256 <= t64) return launch_tiled<T, 256, 256, 8, 2>(p, cus, s);
+  if (t128 <= t64) return launch_tiled<T, 128, 128, 4, 2>(p, cus, s);
   return launch_tiled<T, 64, 64, 4, 4>(p, cus, s);
 }
 

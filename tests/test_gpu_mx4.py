@@ -153,7 +153,8 @@ def check_gemm(a, b, dtype, ends=None, what=""):
 
 GEMM_SIZES = [(1, 8, 32), (1, 16, 256), (1, 1032, 2752), (3, 40, 96), (16, 64, 512), (17, 72, 288), (31, 128, 1024), (33, 256, 160),
               (64, 520, 768), (65, 136, 256), (127, 264, 544), (128, 128, 4096), (200, 8, 320), (257, 264, 64), (300, 520, 1056),
-              (513, 776, 512), (1, 24, 16384), (40, 16, 8192)]
+              (513, 776, 512), (1, 24, 16384), (40, 16, 8192),
+              (2, 8208, 1056), (16, 8200, 800), (30, 8192, 320), (4, 14336, 544), (13, 4096, 2080), (25, 1000, 96)]
 
 
 # enough tiles for the larger tile shapes, with partial tiles on both edges and partial last slices
@@ -197,7 +198,7 @@ ENDS = [([0, 5, 5, 21], 21), ([40], 40), ([3, 3, 3], 3), ([0, 0, 0, 1], 1), ([1,
 
 
 @pytest.mark.parametrize("K", [64, 800])
-@pytest.mark.parametrize("ends, M", ENDS)
+@pytest.mark.parametrize("ends, M", ENDS + [([0, 3, 3, 20, 31], 32), ([2] * 40 + [9], 12), ([16, 16, 16], 16), ([0, 1], 1)])
 def test_gemm_stacked_problems(ends, M, K):
     N = 72 if len(ends) < 20 else 16
     got, want = check_gemm(random_form(1, M, K, 120, 126), random_form(2, N * len(ends), K, 120, 126), "bf16", ends)
