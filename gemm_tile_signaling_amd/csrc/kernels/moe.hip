@@ -35,7 +35,7 @@ struct MoeParams {
   int32_t *ids_out;
   float *wts_out;
   uint32_t *counters;  // [0]: token tiles done; [1 + tile]: router workgroups done; then down's tiles; all zero between calls
-  int32_t *head;       // number of active experts
+  int32_t *head;       // number of active experts; most tokens of one of them
   MoeSlot *slots;
   float *row_w;        // weight of each row of h
   int32_t *ids;
@@ -127,6 +127,7 @@ __device__ __forceinline__ void put(float *p, float v) {
 __device__ __forceinline__ void put(int32_t *p, int32_t v) {
   __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
+constexpr int kCoherent = 0x11;  // the same for buffer loads and stores: sc0 | sc1, system scope
 template <typename V>
 __device__ __forceinline__ V get(const V *p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -168,18 +169,18 @@ __device__ __forceinline__ void select_token(const MoeParams &p, int lane, Load 
 #pragma unroll
     for (int i = 0; i < R; ++i) best = max(best, key[i]);
     best = wave_max(best);
-    int at = -1;  // lowest index that holds it
+    int at = 0;  // lowest index that holds it
     float le = 0;
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
+    for (int i = R - 1; i >= 0; --i) {
       const uint64_t has = __ballot(key[i] == best);
-      if (at < 0 && has) {
-        const int src = __builtin_ctzll(has);
-        at = i * 64 + src;
-        le = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(l[i]), src));
-        if (lane == src) key[i] = 0;
-      }
+      const int src = __builtin_ctzll(has | 1ull << 63);
+      const float there = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(l[i]), src));
+      at = has ? i * 64 + src : at;
+      le = has ? there : le;
     }
+#pragma unroll
+    for (int i = 0; i < R; ++i) key[i] = i * 64 + lane == at ? 0u : key[i];
     if (j == 0) {
       top = le;
 #pragma unroll
@@ -284,6 +285,8 @@ __global__ __launch_bounds__(64 * kRouterWaves) void moe_router(MoeParams p) {
       select_token<1>(p, lane, [&](int e) { return tile_logits[wave][e]; }, &id, &w);
     else if (p.E <= 64)
       select_token<1>(p, lane, far, &id, &w);
+    else if (p.E <= 128)
+      select_token<2>(p, lane, far, &id, &w);
     else if (p.E <= 256)
       select_token<4>(p, lane, far, &id, &w);
     else
@@ -316,11 +319,13 @@ __global__ __launch_bounds__(64 * kRouterWaves) void moe_router(MoeParams p) {
   __syncthreads();
   if (wave == 0) {
     int n = 0, row = 0;
+    uint32_t most_tokens = 0;
     for (int b = 0; b < p.local; b += 64) {
       const uint64_t m = b + lane < p.local ? mask[b + lane] : 0;
       const uint64_t any = __ballot(m != 0);
       if (!any) continue;
       const int count = __popcll(m);
+      most_tokens = max(most_tokens, (uint32_t)count);
       int before = count;  // rows of the lanes up to this one
 #pragma unroll
       for (int d = 1; d < 64; d *= 2) {
@@ -335,7 +340,11 @@ __global__ __launch_bounds__(64 * kRouterWaves) void moe_router(MoeParams p) {
       row += __shfl(before, 63);
     }
     for (int i = n + lane; i < p.most; i += 64) p.slots[i] = MoeSlot{-1, 0, 0};
-    if (lane == 0) p.head[0] = n;
+    most_tokens = wave_max(most_tokens);
+    if (lane == 0) {
+      p.head[0] = n;
+      p.head[1] = (int32_t)most_tokens;
+    }
   }
   __syncthreads();
   for (int i = tid; i < picks; i += kThreads) {
@@ -629,6 +638,31 @@ __global__ __launch_bounds__(64 * kUpWaves, 2) void moe_up(MoeParams p) {
   }
 }
 
+// The parts of ROWS outputs from d0 on, of every token, added up in their order.
+// Four outputs a thread, eight parts under way at a time: the parts come from
+// memory, and one workgroup reads them all.
+template <typename T, int ROWS, int THREADS>
+__device__ __forceinline__ void join_parts(const MoeParams &p, int d0) {
+  const uint32_t bytes = (uint32_t)p.T * (uint32_t)p.D * 4u;
+  for (int i = threadIdx.x; i < p.T * (ROWS / 4); i += THREADS) {
+    const int t = i / (ROWS / 4), d = d0 + i % (ROWS / 4) * 4;
+    if (d >= p.D) continue;
+    f32x4 v = {};
+    for (int s = 0; s < p.splits; s += 8) {
+      f32x4 x[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const __amdgpu_buffer_rsrc_t r =
+            make_rsrc(p.partial + (int64_t)(s + q) * p.T * p.D, s + q < p.splits ? bytes : 0u);  // past the last one: zeros
+        x[q] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (uint32_t)(t * p.D + d) * 4u, 0, kCoherent));
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v += x[q];
+    }
+    *reinterpret_cast<u32x2 *>(p.out + (int64_t)t * p.D + d) = pack4<T>(v);
+  }
+}
+
 // Down: 16 RB outputs of every token per workgroup; the waves of `splits`
 // workgroups share the active experts' ffn evenly, an expert after the other.
 // h comes as pairs of 16-bit values, [row][2][F] (F in panels with 4-bit weights).
@@ -644,6 +678,8 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void moe_down(MoeParams p) {
   const int d0 = blockIdx.x * 16 * RB, rows = min(16 * RB, p.D - d0);
   constexpr int KU = MX4 ? 256 : 128;
   const int units = (p.F + KU - 1) / KU;
+  // the first 64 active experts, one a lane: their loads and the count's are under way together
+  const MoeSlot mine64 = p.slots[min(lane, p.most - 1)];
   const int64_t total = (int64_t)p.head[0] * units;
   const int part = blockIdx.y * kDownWaves + wave, parts = p.splits * kDownWaves;
   int64_t u = total * part / parts;
@@ -654,7 +690,15 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void moe_down(MoeParams p) {
     const int at = (int)(u / units), first = (int)(u - (int64_t)at * units);
     const int last = (int)min((int64_t)units, first + (u_end - u));
     u += last - first;
-    const MoeSlot slot = p.slots[at];
+    MoeSlot slot;
+    if (at < 64) {
+      slot.expert = __builtin_amdgcn_readlane(mine64.expert, at);
+      slot.row = __builtin_amdgcn_readlane(mine64.row, at);
+      slot.mask = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(mine64.mask >> 32), at) << 32 |
+                  (uint32_t)__builtin_amdgcn_readlane((int)mine64.mask, at);
+    } else {
+      slot = p.slots[at];
+    }
     const int e = __builtin_amdgcn_readfirstlane(slot.expert), n = __builtin_amdgcn_readfirstlane(__popcll(slot.mask));
     const int64_t row0 = (int64_t)e * p.D + d0;
     auto work = [&](auto ctc, int base) {
@@ -666,6 +710,12 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void moe_down(MoeParams p) {
         const int rank = DENSE ? __popcll(slot.mask & ((1ull << t) - 1)) : base + t;
         const bool has = DENSE ? (slot.mask >> t & 1) : rank < n;
         col[c] = has ? (uint32_t)(rank * 2 + j / TOKENS) * h_row : kOutOfRange;
+      }
+      float token_w[TT];  // asked for here, used after the products
+#pragma unroll
+      for (int c = 0; c < TT; ++c) {
+        const int t = c * 16 + r, rank = __popcll(slot.mask & ((1ull << t) - 1));
+        token_w[c] = slot.mask >> t & 1 ? p.row_w[slot.row + rank] : 0.0f;
       }
       f32x4 acc[RB][CT] = {};
       const uint16_t *h = p.h + (int64_t)slot.row * h_row;
@@ -691,7 +741,6 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void moe_down(MoeParams p) {
       for (int c = 0; c < TT; ++c) {
         const int t = c * 16 + r, rank = __popcll(slot.mask & ((1ull << t) - 1)), pos = rank - base;
         const bool mine = (slot.mask >> t & 1) && pos >= 0 && pos < TOKENS;
-        const float w = mine ? p.row_w[slot.row + rank] : 0.0f;
 #pragma unroll
         for (int i = 0; i < RB; ++i)
 #pragma unroll
@@ -705,7 +754,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void moe_down(MoeParams p) {
                 v = pos >= 16 ? o : v;
               }
             }
-            if (mine) sum[i][c][q] += w * v;
+            if (mine) sum[i][c][q] += token_w[c] * v;
           }
       }
     };
@@ -743,42 +792,298 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void moe_down(MoeParams p) {
   if (p.splits == 1) return;
   // the last of the tile's workgroups adds the parts up, in their order
   if (!arrive_last(&p.counters[8 + blockIdx.x], p.splits)) return;
-  for (int i = tid; i < p.T * 16 * RB; i += 64 * kDownWaves) {
-    const int t = i / (16 * RB), d = d0 + i % (16 * RB);
-    if (d >= p.D) continue;
-    float v = 0;
-    for (int s = 0; s < p.splits; ++s) v += get(&p.partial[((int64_t)s * p.T + t) * p.D + d]);
-    reinterpret_cast<T *>(p.out)[(int64_t)t * p.D + d] = (T)v;
-  }
+  join_parts<T, 16 * RB, 64 * kDownWaves>(p, d0);
 }
 
-template <typename T, bool MX4, int RBU, int CTU, int RBD, bool DENSE, int TT>
-int launch_sized(MoeParams p, int cus, hipStream_t s) {
+// Down for more than a few tokens: there every wave's own reading of h would be
+// more than its weights (from L2, but through the same loads).  Here the waves
+// split the rows instead, 16 RB each, and share a stage of h in LDS: KU values of
+// every column of the expert at hand.  Stage and weights of the next unit are
+// loaded while a unit is multiplied, one barrier a unit.  The workgroups of a
+// row tile share the active experts' ffn evenly as in moe_down.
+constexpr int kWideWaves = 8;
+template <bool MX4>
+struct DownWide {
+  static constexpr int RB = MX4 ? 2 : 1, ROWS = kWideWaves * 16 * RB;
+  static constexpr int KU = MX4 ? 512 : 256;   // values of k a unit
+  static constexpr int COLB = KU * 2, CHUNKS = COLB / 16;  // bytes and 16-byte chunks of a staged column
+  static constexpr int stage(int ct) { return ct * 16 * COLB; }
+};
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+template <typename T, bool MX4, int TT>
+__global__ __launch_bounds__(64 * kWideWaves, 2) void moe_down_wide(MoeParams p) {
+  using C = std::conditional_t<MX4, __bf16, T>;
+  using W = DownWide<MX4>;
+  constexpr int RB = W::RB, KU = W::KU;
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
+  const int d0 = blockIdx.x * W::ROWS + wave * 16 * RB;  // this wave's rows
+  const uint32_t rows = (uint32_t)max(0, min(16 * RB, p.D - d0));
+  const int units = (p.F + KU - 1) / KU;
+  const MoeSlot mine64 = p.slots[min(lane, p.most - 1)];
+  const int active = __builtin_amdgcn_readfirstlane(p.head[0]), most_tokens = __builtin_amdgcn_readfirstlane(p.head[1]);
+  const int total = active * units;
+  const int u0 = (int)((int64_t)total * blockIdx.y / p.splits), u1 = (int)((int64_t)total * (blockIdx.y + 1) / p.splits);
+  const uint32_t pitch = MX4 ? (uint32_t)p.F / 2u : (uint32_t)p.F * 2u;
+  const int64_t h_row = MX4 ? panels_of(p.F) : p.F;
+  auto slot_at = [&](int at) {
+    MoeSlot slot;
+    if (at < 64) {
+      slot.expert = __builtin_amdgcn_readlane(mine64.expert, at);
+      slot.row = __builtin_amdgcn_readlane(mine64.row, at);
+      slot.mask = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(mine64.mask >> 32), at) << 32 |
+                  (uint32_t)__builtin_amdgcn_readlane((int)mine64.mask, at);
+    } else {
+      slot = p.slots[at];
+      slot.expert = __builtin_amdgcn_readfirstlane(slot.expert);
+    }
+    return slot;
+  };
+  f32x4 sum[RB][TT] = {};
+  // 8 CT tokens of each expert, from the one of rank `base` on
+  auto pass = [&](auto ctc, int base) {
+    constexpr int CT = decltype(ctc)::value, TOKENS = kPairTokens<CT>, L = KU / 32;
+    constexpr int NWT = MX4 ? KU / 256 * 2 : L;  // weight loads of a row block and unit
+    u32x4 a[RB][NWT];
+    uint32_t sc[RB][MX4 ? KU / 256 : 1];
+    auto issue = [&](const MoeSlot &slot, int unit, int buf) {
+      const int n = __popcll(slot.mask), k0 = unit * KU;
+      const __amdgpu_buffer_rsrc_t rh = make_rsrc(p.h + (int64_t)slot.row * 2 * h_row, (uint32_t)(n * 4 * h_row));
+      // columns: instruction q of wave w fills 1 KiB; chunk c of column j lies at c ^ (j % 16)
+#pragma unroll
+      for (int q = 0; q < W::stage(CT) / 1024 / kWideWaves; ++q) {
+        const int at = (q * kWideWaves + wave) * 64 + lane, j = at / W::CHUNKS, c = (at % W::CHUNKS) ^ (j & 15);
+        const int rank = base + j % TOKENS, plane = j / TOKENS;
+        // values past the row's end are not loaded (with 4-bit weights by their block, see panel_place)
+        const bool inside = MX4 ? k0 / 32 + c / 32 * 8 + (c & 3) * 2 + (c >> 4 & 1) < p.F / 32 : k0 + c * 8 < p.F;
+        const uint32_t from = (uint32_t)((rank * 2 + plane) * h_row + k0) * 2u + c * 16u;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            rh, (lds_void *)(smem + buf * W::stage(CT) + (q * kWideWaves + wave) * 1024), 16,
+            rank < n && inside ? from : kOutOfRange, 0, 0, 0);
+      }
+      const int64_t row0 = (int64_t)slot.expert * p.D + d0;
+      const __amdgpu_buffer_rsrc_t rw = make_rsrc(p.down + row0 * pitch, rows * pitch);
+      if constexpr (MX4) {
+        const int nb = p.F / 32;
+#pragma unroll
+        for (int s = 0; s < KU / 256; ++s) {
+          const int b = k0 / 32 + s * 8 + g * 2;
+          const __amdgpu_buffer_rsrc_t rs =
+              make_rsrc(p.down_s + (int64_t)(k0 / 256 + s) * p.local * p.D * 8 + row0 * 8, k0 + s * 256 < p.F ? rows * 8 : 0);
+#pragma unroll
+          for (int i = 0; i < RB; ++i) {
+            const uint32_t row = (uint32_t)(i * 16 + r);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              a[i][s * 2 + h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                              rw, b + h < nb ? row * pitch + (b + h) * 16u : kOutOfRange, 0, 0));
+            sc[i][s] = __builtin_amdgcn_raw_buffer_load_b16(rs, row * 8u + g * 2u, 0, 0);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int s = 0; s < L; ++s) {
+          const int k = k0 + s * 32 + g * 8;
+#pragma unroll
+          for (int i = 0; i < RB; ++i)
+            a[i][s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                    rw, k < p.F ? (uint32_t)(i * 16 + r) * pitch + k * 2u : kOutOfRange, 0, 0));
+        }
+      }
+    };
+    // the first unit at or after u whose expert has tokens in this pass
+    MoeSlot slot{};
+    int held = -1;
+    auto seek = [&](int u) {
+      for (; u < u1; ++u) {
+        const int at = u / units;
+        if (at != held) {
+          slot = slot_at(at);
+          held = at;
+        }
+        if (__popcll(slot.mask) > base) break;
+        u = (at + 1) * units - 1;
+      }
+      return min(u, u1);
+    };
+    f32x4 acc[RB][CT] = {};
+    int u = seek(u0), buf = 0;
+    if (u >= u1) return;
+    __syncthreads();  // the last pass's readers are through
+    issue(slot, u % units, buf);
+    for (;;) {
+      __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0), lgkmcnt(0): the unit's stage and weights, and the reads of the other stage
+      __syncthreads();
+      u32x4 w[RB][NWT];
+      float f[RB][MX4 ? KU / 128 : 1];
+      const MoeSlot cur = slot;
+      const int cur_at = u / units, cur_k = (u % units) * KU;
+#pragma unroll
+      for (int i = 0; i < RB; ++i) {
+#pragma unroll
+        for (int s = 0; s < NWT; ++s) w[i][s] = a[i][s];
+        if constexpr (MX4)
+#pragma unroll
+          for (int s = 0; s < KU / 128; ++s)
+            f[i][s] = mx4_scale(cur_k / 32 + s / 2 * 8 + g * 2 + s % 2 < p.F / 32 ? sc[i][s / 2] >> (8 * (s % 2)) & 255u : 127u);
+      }
+      const int next = seek(u + 1);
+      if (next < u1) issue(slot, next % units, buf ^ 1);
+      const char *stage = smem + buf * W::stage(CT);
+#pragma unroll
+      for (int s = 0; s < L; ++s) {
+        u32x4 x[CT];
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+          x[c] = *reinterpret_cast<const u32x4 *>(stage + (c * 16 + r) * W::COLB + ((s * 4 + g) ^ r) * 16);
+#pragma unroll
+        for (int i = 0; i < RB; ++i) {
+          u32x4 v;
+          if constexpr (MX4)  // place 4 (8 s' + 4 h + j): panel s', half h, dword j
+            v = mx4_to_bf16(w[i][s / 8 * 2 + s / 4 % 2][s % 4], f[i][s / 8 * 2 + s / 4 % 2]);
+          else
+            v = w[i][s];
+#pragma unroll
+          for (int c = 0; c < CT; ++c) acc[i][c] = mma16<C>(v, x[c], acc[i][c]);
+        }
+      }
+      if (next >= u1 || next / units != cur_at) {
+        // the expert's share is done: to its own tokens only, so that a NaN or an
+        // infinity in its weights stays with them
+        fold(acc);
+#pragma unroll
+        for (int c = 0; c < TT; ++c) {
+          const int t = c * 16 + r, rank = __popcll(cur.mask & ((1ull << t) - 1)), pos = rank - base;
+          const bool mine = (cur.mask >> t & 1) && pos >= 0 && pos < TOKENS;
+          const float weight = mine ? p.row_w[cur.row + rank] : 0.0f;
+#pragma unroll
+          for (int i = 0; i < RB; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int from = (pos & 15) + g * 16;
+              float v = __shfl(acc[i][0][q], from);
+              if constexpr (CT > 2) {
+                const float o = __shfl(acc[i][1][q], from);
+                v = pos >= 16 ? o : v;
+              }
+              if (mine) sum[i][c][q] += weight * v;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < RB; ++i)
+#pragma unroll
+          for (int c = 0; c < CT; ++c) acc[i][c] = f32x4{};
+      }
+      if (next >= u1) return;
+      u = next;
+      buf ^= 1;
+    }
+  };
+  using std::integral_constant;
+  if (most_tokens <= 8) {
+    pass(integral_constant<int, 1>{}, 0);
+  } else if (TT == 1 || most_tokens <= 16) {
+    pass(integral_constant<int, 2>{}, 0);
+  } else if constexpr (TT > 1) {
+    // past 32 tokens of one expert its rows are read again
+    for (int base = 0; base < most_tokens; base += 32) pass(integral_constant<int, 4>{}, base);
+  }
+  // lane: 4 neighbouring outputs of token 16 c + r; a part goes out in 16-byte pieces,
+  // written through like put()
+  const __amdgpu_buffer_rsrc_t rp =
+      make_rsrc(p.partial + (int64_t)blockIdx.y * p.T * p.D, (uint32_t)p.T * (uint32_t)p.D * 4u);
+#pragma unroll
+  for (int c = 0; c < TT; ++c)
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+      const int t = c * 16 + r, d = d0 + i * 16 + g * 4;
+      if (t >= p.T || d >= p.D) continue;
+      if (p.splits == 1)
+        *reinterpret_cast<u32x2 *>(p.out + (int64_t)t * p.D + d) = pack4<T>(sum[i][c]);
+      else
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, sum[i][c]), rp, (uint32_t)(t * p.D + d) * 4u, 0,
+                                               kCoherent);
+    }
+  if (p.splits == 1) return;
+  if (!arrive_last(&p.counters[8 + blockIdx.x], p.splits)) return;
+  join_parts<T, W::ROWS, 64 * kWideWaves>(p, blockIdx.x * W::ROWS);
+}
+
+template <typename T, bool MX4, int RBU, int CTU>
+int launch_first(const MoeParams &p, hipStream_t s) {
   // workgroups that lay the tokens out: 8 values a thread
   const int lay = MX4 ? (p.T * (p.D / 8) + 64 * kRouterWaves - 1) / (64 * kRouterWaves) : 0;
   moe_router<T><<<p.expert_wgs * p.tiles + lay, 64 * kRouterWaves, 0, s>>>(p);
   if (hipGetLastError() != hipSuccess) return FO_ERR_HIP;
   moe_up<T, MX4, RBU, CTU><<<dim3((p.F + 16 * RBU - 1) / (16 * RBU), p.most), 64 * kUpWaves, 0, s>>>(p);
-  if (hipGetLastError() != hipSuccess) return FO_ERR_HIP;
-  // a workgroup for every CU, as long as every wave has a few steps of K
-  const int tiles = (p.D + 16 * RBD - 1) / (16 * RBD), units = (p.F + 255) / 256;
-  int splits = (cus + tiles - 1) / tiles;
-  const int64_t most = (int64_t)p.most * units / (kDownWaves * 2);
-  if (splits > most) splits = (int)most;
-  if (splits > kMoeMaxSplits) splits = kMoeMaxSplits;
-  p.splits = splits < 1 ? 1 : splits;
-  moe_down<T, MX4, RBD, DENSE, TT><<<dim3(tiles, p.splits), 64 * kDownWaves, 0, s>>>(p);
   return hipGetLastError() == hipSuccess ? FO_OK : FO_ERR_HIP;
 }
 
+// Workgroups that share a tile of outputs: one for every CU, as long as each has `least` units of work.
+int splits_of(const MoeParams &p, int cus, int tiles, int64_t units, int64_t least) {
+  int64_t splits = (cus + tiles - 1) / tiles;
+  if (splits > p.most * units / least) splits = p.most * units / least;
+  if (splits > kMoeMaxSplits) splits = kMoeMaxSplits;
+  return splits < 1 ? 1 : (int)splits;
+}
+
+template <typename T, bool MX4, int RB, bool DENSE, int TT>
+int launch_down(MoeParams p, int cus, hipStream_t s) {
+  const int tiles = (p.D + 16 * RB - 1) / (16 * RB);
+  p.splits = splits_of(p, cus, tiles, (p.F + 255) / 256, kDownWaves * 2);
+  moe_down<T, MX4, RB, DENSE, TT><<<dim3(tiles, p.splits), 64 * kDownWaves, 0, s>>>(p);
+  return hipGetLastError() == hipSuccess ? FO_OK : FO_ERR_HIP;
+}
+
+template <typename T, bool MX4, int TT>
+int launch_down_wide(MoeParams p, int cus, hipStream_t s) {
+  using W = DownWide<MX4>;
+  constexpr int kLds = 2 * W::stage(TT > 1 ? 4 : 2);
+  const auto kernel = &moe_down_wide<T, MX4, TT>;
+  static bool configured = false;  // per process; the attribute is per kernel and device-independent
+  if (!configured) {
+    if (hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, kLds) !=
+        hipSuccess)
+      return FO_ERR_HIP;
+    configured = true;
+  }
+  const int tiles = (p.D + W::ROWS - 1) / W::ROWS;
+  p.splits = splits_of(p, cus, tiles, (p.F + W::KU - 1) / W::KU, 2);
+  kernel<<<dim3(tiles, p.splits), 64 * kWideWaves, kLds, s>>>(p);
+  return hipGetLastError() == hipSuccess ? FO_OK : FO_ERR_HIP;
+}
+
+// Which kernels.  Two forms of the second product: every wave on its own
+// (moe_down), or h shared through LDS (moe_down_wide).  Sharing pays once an
+// expert has some tokens (3 of them in the mean) and, with 4-bit weights, where
+// there is enough to read (2^28 values) to make up for its fewer, longer parts.  Measured
+// (own / shared, us): 16-bit, 64 tokens on 8 experts of 4096 x 14336 737 / 205, on 125
+// of 2048 x 768 179 / 90, 13 tokens on 71 of them 47 / 53; 4-bit, 16 tokens on 8 of 4096 x
+// 14336 98 / 62, 64 tokens on 126 of 2048 x 768 47 / 61, on 8 of 2048 x 1408 12 / 23.
+// The first product takes 32 values of h a workgroup instead of 16 with 4-bit weights
+// from 2^27 values on (126 of 2048 x 768: 60 -> 50 us; 8 of 2048 x 1408: 13.7 -> 14.4).
 template <typename T, bool MX4>
 int launch_typed(const MoeParams &p, int cus, hipStream_t s) {
   constexpr int X = MX4 && std::is_same_v<T, _Float16> ? 2 : 1;  // columns of a token in the first product
-  if (p.T <= 4) return launch_sized<T, MX4, 1, 1, 1, true, 1>(p, cus, s);
-  if (p.T <= 8) return launch_sized<T, MX4, 2, 1, 2, true, 1>(p, cus, s);
-  if (p.T <= 16) return launch_sized<T, MX4, 2, X, 2, false, 1>(p, cus, s);
-  if (p.T <= 32) return launch_sized<T, MX4, 2, 2 * X, 2, false, 2>(p, cus, s);
-  return launch_sized<T, MX4, 2, 4, 2, false, 4>(p, cus, s);
+  const int64_t values = (int64_t)p.most * p.D * p.F;
+  const bool big = MX4 && values >= (1ll << 27);
+  const bool shared = (int64_t)p.T * p.top_k >= 3ll * p.E && (!MX4 || values >= (1ll << 28));
+  if (p.T <= 8) {
+    if (const int rc = launch_first<T, MX4, 1, X>(p, s)) return rc;
+    return launch_down<T, MX4, 1, true, 1>(p, cus, s);
+  }
+  if (p.T <= 16) {
+    if (const int rc = big ? launch_first<T, MX4, 2, X>(p, s) : launch_first<T, MX4, 1, X>(p, s)) return rc;
+    return shared ? launch_down_wide<T, MX4, 1>(p, cus, s) : launch_down<T, MX4, 1, false, 1>(p, cus, s);
+  }
+  if (p.T <= 32) {
+    if (const int rc = big ? launch_first<T, MX4, 2, 2 * X>(p, s) : launch_first<T, MX4, 1, 2 * X>(p, s)) return rc;
+    return shared ? launch_down_wide<T, MX4, 2>(p, cus, s) : launch_down<T, MX4, 1, false, 2>(p, cus, s);
+  }
+  if (const int rc = big ? launch_first<T, MX4, 2, 4>(p, s) : launch_first<T, MX4, 1, 4>(p, s)) return rc;
+  return shared ? launch_down_wide<T, MX4, 4>(p, cus, s) : launch_down<T, MX4, 1, false, 4>(p, cus, s);
 }
 
 }  // namespace

@@ -18,12 +18,12 @@ int launch_mx4_gemm(const void *a_codes, const void *a_scales, const void *b_cod
                     int cus, hipStream_t s);
 
 // Most workgroups that share one tile of a layer's outputs.
-constexpr int kMoeMaxSplits = 16;
+constexpr int kMoeMaxSplits = 32;
 
 // Parts of a layer's workspace, as byte offsets; each begins on 256 bytes.
 struct MoeLayout {
   int64_t counters;  // u32 [8 + outputs / 16]: workgroups done; zero between calls
-  int64_t head;      // int32: number of active experts
+  int64_t head;      // int32 [2]: number of active experts, most tokens of one of them
   int64_t slots;     // 16 bytes for each expert that can be active
   int64_t row_w;     // float [max_tokens * top_k]: weight of each row of h
   int64_t ids;       // int32 [max_tokens][top_k]: picked experts
@@ -46,7 +46,7 @@ inline MoeLayout moe_layout(const fo_moe_desc &d) {
   auto whole = [](int64_t k) { return (k + 255) / 256 * 256; };
   const int64_t picks = (int64_t)d.max_tokens * d.top_k;
   l.counters = take(4 * (8 + (d.hidden + 15) / 16));
-  l.head = take(4);
+  l.head = take(8);
   l.slots = take(16 * (picks < d.local_experts ? picks : d.local_experts));
   l.row_w = take(4 * picks);
   l.ids = take(4 * picks);

@@ -141,6 +141,23 @@ def test_layer(T, D, F, E, k, first, local, weights, dtype):
         assert not c.run()[0][~held].any()             # nothing held here: zeros
 
 
+@pytest.mark.parametrize("T, D, F, E, k, first, local, weights", [
+    # enough values for the forms that large 4-bit experts take; 9 .. 64 tokens of one expert, a share, odd panels
+    (16, 2080, 3232, 40, 8, 0, 40, "mx4"), (24, 2048, 4160, 33, 5, 1, 32, "mx4"), (64, 4096, 8224, 8, 2, 0, 8, "mx4"),
+    (12, 2048, 4128, 18, 6, 0, 18, "mx4"), (64, 1024, 776, 8, 4, 0, 8, "16"), (40, 520, 264, 9, 3, 3, 4, "16")])
+def test_large_experts(T, D, F, E, k, first, local, weights):
+    c = Case(T, D, F, E, k, first, local, weights, "bf16" if T % 3 else "fp16", renorm=T % 2 == 0, seed=9)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("weights", ["16", "mx4"])
+@pytest.mark.parametrize("T", [9, 33, 64])
+def test_every_token_on_every_expert(T, weights):
+    """top_k == experts: every expert has all the tokens (two passes over its rows past 32)."""
+    c = Case(T, 256, 544, 3, 3, weights=weights)
+    c.check(c.run())
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("T, D, F, E, k", [(3, 8, 8, 4, 2), (18, 72, 40, 9, 3), (64, 1000, 776, 4, 1), (1, 24, 2056, 7, 7)])
 def test_sizes_that_are_multiples_of_8_only(T, D, F, E, k, dtype):
