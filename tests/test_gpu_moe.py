@@ -141,13 +141,81 @@ def test_layer(T, D, F, E, k, first, local, weights, dtype):
         assert not c.run()[0][~held].any()             # nothing held here: zeros
 
 
-@pytest.mark.parametrize("T, D, F, E, k, first, local, weights", [
-    # enough values for the forms that large 4-bit experts take; 9 .. 64 tokens of one expert, a share, odd panels
-    (16, 2080, 3232, 40, 8, 0, 40, "mx4"), (24, 2048, 4160, 33, 5, 1, 32, "mx4"), (64, 4096, 8224, 8, 2, 0, 8, "mx4"),
-    (12, 2048, 4128, 18, 6, 0, 18, "mx4"), (64, 1024, 776, 8, 4, 0, 8, "16"), (40, 520, 264, 9, 3, 3, 4, "16")])
-def test_large_experts(T, D, F, E, k, first, local, weights):
-    c = Case(T, D, F, E, k, first, local, weights, "bf16" if T % 3 else "fp16", renorm=T % 2 == 0, seed=9)
-    c.check(c.run())
+def device_case(T, D, F, E, k, first, local, weights, dtype, renorm, seed):
+    """Inputs made on the device, and the layer in 64 bits with the error bound of the module's docstring, there as well."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    normal = lambda *sh: torch.randn(*sh, generator=g, device="cuda")  # noqa: E731
+    x, router = normal(T, D).to(TORCH[dtype]), (normal(E, D) * D ** -0.5).to(TORCH[dtype])
+    mats, values = [], []
+    for rows, cols in ((local * 2 * F, D), (local * D, F)):
+        if weights == "16":
+            w = (normal(rows, cols) * cols ** -0.5).to(TORCH[dtype])
+            mats.append(w)
+            values.append(lambda lo, hi, w=w: w[lo:hi].double())
+        else:
+            nb = cols // 32
+            codes = torch.randint(0, 256, (rows, cols // 2), generator=g, device="cuda", dtype=torch.uint8)
+            scales = torch.randint(118, 122, ((nb + 7) // 8, rows, 8), generator=g, device="cuda", dtype=torch.uint8)
+            if nb % 8:
+                scales[-1, :, nb % 8:] = 255
+            mats.append((codes, scales))
+            table = torch.tensor(np.concatenate([mx4.MAGNITUDES, -mx4.MAGNITUDES]), device="cuda")
+
+            def part(lo, hi, codes=codes, scales=scales, nb=nb, table=table):
+                c = codes[lo:hi].int()
+                v = torch.stack([table[c & 15], table[c >> 4]], -1).reshape(hi - lo, nb, 32)
+                e = scales[:, lo:hi].permute(1, 0, 2).reshape(hi - lo, -1)[:, :nb].double() - 127
+                return (v * torch.exp2(e)[..., None]).reshape(hi - lo, -1)
+            values.append(part)
+    layer = fo.Moe(D, F, E, k, dtype=dtype, weights=weights, renormalize=renorm, first_expert=first, local_experts=local)
+    ids = torch.empty(T, k, dtype=torch.int32, device="cuda")
+    wts = torch.empty(T, k, dtype=torch.float32, device="cuda")
+    out = layer.forward(x, router, *mats, layer.new_workspace(), picks=(ids, wts))
+    xd, rd = x.double(), router.double()
+    logits = xd @ rd.t()
+    dl = (D * U * (xd.abs() @ rd.abs().t())).amax(1, keepdim=True)
+    order = logits.gather(1, ids.long())
+    assert (order[:, :-1] - order[:, 1:] >= -2 * dl).all()
+    assert (order[:, -1:] - logits.scatter(1, ids.long(), -float("inf")) >= -2 * dl).all()
+    p = torch.exp(logits - logits.amax(1, keepdim=True))
+    w = p.gather(1, ids.long())
+    w = w / (w.sum(1, keepdim=True) if renorm else p.sum(1, keepdim=True))
+    rel = 4 * dl + ((order - logits.amax(1, keepdim=True)).abs() + E + 4) * U
+    want, bound = torch.zeros_like(xd), torch.zeros_like(xd)
+    pair = 2.0 ** -25 if dtype == "fp16" and weights == "16" else 0.0
+    for e in range(local):
+        t, j = (ids == first + e).nonzero(as_tuple=True)
+        if t.numel() == 0:
+            continue
+        gu = values[0](e * 2 * F, (e + 1) * 2 * F)
+        gate, up = (xd[t] @ gu.t()).split(F, 1)
+        da, du = (D * U * (xd[t].abs() @ gu.abs().t())).split(F, 1)
+        del gu
+        s = gate / (1 + torch.exp(-gate))
+        h = s * up
+        dh = 1.1 * up.abs() * da + s.abs() * du + h.abs() * ((gate.abs() + 8) * U + 2.0 ** -16) + pair
+        dn = values[1](e * D, (e + 1) * D)
+        y = h @ dn.t()
+        dy = dh @ dn.abs().t() + (F + 32) * U * (h.abs() @ dn.abs().t()) + rel[t, j, None] * y.abs()
+        want.index_add_(0, t, w[t, j, None] * y)
+        bound.index_add_(0, t, w[t, j, None] * dy)
+    bits = oracle.DTYPES[dtype]["p"]
+    bound += 2.0 ** -bits * (want.abs() + bound) + 2.0 ** (-133 if dtype == "bf16" else -25)
+    bad = (out.double() - want).abs() > bound
+    assert not bad.any(), (int(bad.sum()), bad.nonzero()[:3].tolist(), float((out.double() - want).abs().max()))
+
+
+@pytest.mark.parametrize("T, D, F, E, k, first, local, weights, dtype", [
+    # enough values for the forms that large 4-bit experts take: a few, some and all tokens on an expert (past 16 and
+    # 32 of them the columns take more tiles and a second pass), partial panels, a share of the experts
+    (16, 2080, 3232, 40, 8, 0, 40, "mx4", "fp16"), (24, 2048, 4160, 33, 5, 1, 32, "mx4", "bf16"),
+    (64, 4096, 8224, 8, 2, 0, 8, "mx4", "bf16"), (64, 2080, 16160, 8, 8, 0, 8, "mx4", "fp16"),
+    (30, 4096, 14336, 5, 5, 0, 5, "mx4", "bf16"), (12, 2048, 4128, 36, 12, 0, 36, "mx4", "bf16"),
+    (64, 4096, 4104, 8, 4, 0, 8, "16", "bf16"), (40, 2056, 1032, 9, 3, 3, 4, "16", "fp16"),
+    (3, 4096, 14336, 4, 2, 0, 4, "16", "bf16"), (8, 4096, 4096, 16, 2, 0, 16, "mx4", "fp16")])
+def test_large_experts(T, D, F, E, k, first, local, weights, dtype):
+    say(f"moe large T={T} D={D} F={F} E={E} k={k} first={first} local={local} {weights} {dtype}")
+    device_case(T, D, F, E, k, first, local, weights, dtype, T % 2 == 0, T + D)
 
 
 @pytest.mark.parametrize("weights", ["16", "mx4"])
