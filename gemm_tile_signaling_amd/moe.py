@@ -11,7 +11,7 @@ import ctypes as C
 from typing import Optional
 
 from . import _DTYPES
-from .mx4 import _buffer, _device, _done, _new, _on_stream, _ops, mx4_shapes
+from .mx4 import _buffer, _device, _done, _new, _of_type, _on_stream, _ops, mx4_shapes
 
 __all__ = ["Moe"]
 
@@ -74,6 +74,7 @@ class Moe:
     def _matrix(self, m, name: str, numel, device: int):
         """(address, address of the scales or None) of one of the experts' matrices."""
         if len(numel) == 1:
+            _of_type(m, name, _ops().types[self.dtype])
             return _sized(m, name, numel[0], 2, device), None
         codes, scales = m
         return _sized(codes, name, numel[0], 1, device), _sized(scales, name, numel[1], 1, device)
@@ -94,6 +95,9 @@ class Moe:
             raise ValueError(f"x: {tokens} tokens, the layer is for at most {self.max_tokens}")
         if out is None:
             out = _new(x, (tokens, self.hidden), wanted, stream)
+        else:
+            _of_type(out, "out", wanted)
+        _of_type(router, "router", wanted)
         gu, gus = self._matrix(gate_up, "gate_up", self._numel[0], device)
         dn, dns = self._matrix(down, "down", self._numel[1], device)
         ids = wts = None
