@@ -1,0 +1,96 @@
+"""A mixture-of-experts layer served from 4-bit weights: prompts and single tokens from the same tensors.
+
+    python -m examples.moe_mx4 [--hidden 2048 --ffn 1408 --experts 64 --top-k 6 --prompt 512 --tokens 4]
+
+The experts' weights are quantised once.  A prompt's rows are sorted by expert
+and go through two grouped 4-bit products (``mx4_gemm`` with ``row_ends``), the
+activations quantised on the way; a few tokens go through ``Moe.forward``,
+which reads each picked expert's weights once and keeps activations at 16 bits
+or more.  Needs an MI355X; random weights and inputs.
+"""
+
+import argparse
+
+import torch
+
+import gemm_tile_signaling_amd as fo
+
+
+class Mx4Experts:
+    """Router [E, D] and experts' gate_up [E, 2F, D] and down [E, D, F], kept as 4-bit codes and scales."""
+
+    def __init__(self, router, gate_up, down, top_k: int):
+        self.E, rows, self.D = gate_up.shape
+        self.F, self.k, self.router = rows // 2, top_k, router
+        self.dtype = {torch.bfloat16: "bf16", torch.float16: "fp16"}[router.dtype]
+        self.gate_up = fo.mx4_quantize(gate_up.reshape(self.E * rows, self.D))
+        self.down = fo.mx4_quantize(down.reshape(self.E * self.D, self.F))
+        self.layer = fo.Moe(self.D, self.F, self.E, top_k, dtype=self.dtype, weights="mx4")
+        self.workspace = self.layer.new_workspace(router.device)
+
+    def __call__(self, x):
+        return self.few(x) if x.shape[0] <= self.layer.max_tokens else self.many(x)
+
+    def few(self, x):
+        """At most 64 rows: one call, bound by the picked experts' bytes."""
+        return self.layer.forward(x, self.router, self.gate_up, self.down, self.workspace)
+
+    def many(self, x):
+        """Rows sorted by expert on the device; nothing waits for the host."""
+        T = x.shape[0]
+        p = torch.softmax(x.float() @ self.router.float().t(), -1)
+        w, ids = torch.topk(p, self.k)
+        w = w / w.sum(-1, keepdim=True)
+        order = torch.argsort(ids.flatten(), stable=True)
+        ends = torch.bincount(ids.flatten(), minlength=self.E).cumsum(0).to(torch.int32)
+        rows = order // self.k
+        gu = fo.mx4_gemm(*fo.mx4_quantize(x[rows]), *self.gate_up, dtype=self.dtype, row_ends=ends).float()
+        h = (torch.nn.functional.silu(gu[:, :self.F]) * gu[:, self.F:]).to(x.dtype)
+        y = fo.mx4_gemm(*fo.mx4_quantize(h), *self.down, dtype=self.dtype, row_ends=ends).float()
+        back = torch.empty_like(y)
+        back[order] = y * w.flatten()[order, None]
+        return back.view(T, self.k, self.D).sum(1).to(x.dtype)
+
+
+def distance(a, b):
+    """Relative distance in the 2-norm."""
+    return ((a.float() - b.float()).norm() / b.float().norm()).item()
+
+
+def main(argv=None):
+    """Builds a layer, serves a prompt and a few tokens, and returns the relative distances it prints."""
+    ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
+    for name, default in (("hidden", 2048), ("ffn", 1408), ("experts", 64), ("top-k", 6), ("prompt", 512), ("tokens", 4)):
+        ap.add_argument(f"--{name}", type=int, default=default)
+    a = ap.parse_args(argv)
+    D, F, E = a.hidden, a.ffn, a.experts
+    g = torch.Generator(device="cuda").manual_seed(1)
+    normal = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    router = (normal(E, D) * D ** -0.5).bfloat16()
+    gate_up = (normal(E, 2 * F, D) * D ** -0.5).bfloat16()
+    down = (normal(E, D, F) * F ** -0.5).bfloat16()
+    experts = Mx4Experts(router, gate_up, down, a.top_k)
+    kept = sum(t.numel() for m in (experts.gate_up, experts.down) for t in m)
+    print(f"weights: {2 * (gate_up.numel() + down.numel()) / 1e6:.0f} MB in 16 bits, {kept / 1e6:.0f} MB in 4 bits")
+
+    prompt = normal(a.prompt, D).bfloat16()
+    served = experts.many(prompt)
+    tokens = prompt[:a.tokens]
+    few = experts.few(tokens)
+
+    # the same tokens through the layer with the 16-bit weights, and with the 4-bit weights' values in 16 bits
+    wide = fo.Moe(D, F, E, a.top_k)
+    ws = wide.new_workspace()
+    full = wide.forward(tokens, router, gate_up, down, ws)
+    values = [fo.mx4_dequantize(*m, cols) for m, cols in ((experts.gate_up, D), (experts.down, F))]
+    same = wide.forward(tokens, router, *values, ws)
+    found = {"4-bit layer against its weights' values in 16 bits": distance(few, same),
+             "4-bit layer against the 16-bit layer": distance(few, full),
+             "prompt (4-bit activations too) against the 4-bit layer": distance(served[:a.tokens], few)}
+    for what, d in found.items():
+        print(f"{what}: {d:.2e}")
+    return found
+
+
+if __name__ == "__main__":
+    main()

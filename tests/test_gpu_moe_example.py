@@ -1,0 +1,44 @@
+"""The example that serves one layer's 4-bit weights to prompts and to single tokens.
+
+Bounds on the relative distances it reports, from the format.  Values of a
+block are rounded to 3 significant steps: a normal value's error is at most
+1/4 of the distance between neighbours' lower ends, 1/8 to 1/16 of the value
+in the mean square, so one quantised operand moves a product of independent
+normal values by a relative 0.08 to 0.16.  The layer has three products in a
+row on one path (gate and up enter as a product, then down), so its 4-bit
+weights move the result by at most sqrt(3) 0.16 = 0.28, and 4-bit activations
+add as many again.  Against the same values held in 16 bits only roundings
+remain: bf16 outputs, 2^-9 each, and h in 16 bits or more: 2^-7 bounds them.
+"""
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+pytest.importorskip("torch")
+fo = pytest.importorskip("gemm_tile_signaling_amd")
+
+
+@pytest.mark.parametrize("argv", [[], ["--hidden", "512", "--ffn", "288", "--experts", "5", "--top-k", "2",
+                                       "--prompt", "67", "--tokens", "64"]])
+def test_example(argv, capsys):
+    from examples import moe_mx4
+    same, weights, activations = moe_mx4.main(argv).values()
+    assert same <= 2.0 ** -7
+    assert 0.05 <= weights <= 0.28
+    assert 0.05 <= activations <= 0.28
+    assert "MB in 4 bits" in capsys.readouterr().out
+
+
+def test_prompt_rows_do_not_depend_on_their_order():
+    import torch
+    from examples.moe_mx4 import Mx4Experts
+    g = torch.Generator(device="cuda").manual_seed(2)
+    normal = lambda *s: torch.randn(*s, generator=g, device="cuda").half()  # noqa: E731
+    layer = Mx4Experts(normal(6, 256), normal(6, 192, 256) / 16, normal(6, 256, 96) / 10, 2)
+    x = normal(200, 256)
+    out = layer(x)
+    p = torch.randperm(200, generator=g, device="cuda")
+    # the experts' rows are the same bits; the weights, from a 32-bit product in torch, may move by its roundings
+    assert (layer(x[p]) - out[p]).abs().max() <= 2.0 ** -9 * out.abs().max()
+    assert layer(x[:3]).shape == (3, 256)
