@@ -1,4 +1,4 @@
-"""Build libfo.so in-tree with hipcc for gfx950.
+"""Build libfo.so in-tree with hipcc for gfx950, and the binding's extension module beside it.
 
 Every source under csrc/ is compiled on each call (the build is a few
 seconds per file, run in parallel) and linked into
@@ -19,6 +19,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfo.so")
+CALLS = os.path.join(HERE, "_calls.so")
 
 ARCH = "gfx950"
 FLAGS = [
@@ -45,11 +46,33 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _calls() -> str:
+    """The extension module of the ordinary calls (host code against torch's C++ interface)."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    cmd = [shutil.which("g++") or "g++", "-std=c++17", "-O2", "-Wall", "-shared", "-fPIC", "-D__HIP_PLATFORM_AMD__",
+           "-DUSE_ROCM", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I/opt/rocm/include",
+           "-I" + sysconfig.get_paths()["include"]]
+    for d in cpp_extension.include_paths():
+        cmd += ["-isystem", d]
+    cmd += [os.path.join(CSRC, "python", "calls.cpp"), "-o", CALLS + ".tmp", "-L" + cpp_extension.TORCH_LIB_PATH,
+            "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(CALLS + ".tmp", CALLS)
+    return CALLS
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(CSRC, "kernels", "*.hip")))
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        calls = ex.submit(_calls)
         objs = list(ex.map(_compile, srcs))
+        calls.result()
     tmp = LIB + ".tmp"
     cmd = [_hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -57,7 +80,7 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
     if verbose:
-        print(f"built {LIB} from {len(srcs)} sources")
+        print(f"built {LIB} from {len(srcs)} sources, and {os.path.basename(CALLS)}")
     return LIB
 
 

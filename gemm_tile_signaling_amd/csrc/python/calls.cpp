@@ -1,0 +1,169 @@
+// The ordinary calls of the 4-bit operators, from torch tensors straight to the
+// C ABI (include/fo_ops.h): an extension module, since for kernels of a few
+// microseconds the interpreter's share of a call is as long as the kernel.
+//
+// "Ordinary" is a call whose tensors are contiguous, of the right types and
+// shapes and on the current device, and whose outputs are to be made.  Each
+// function returns the outputs, or None when it finds anything else, before it
+// has enqueued anything; the caller's own checks then name the fault, or take
+// the call.  The library is not linked: bind() is given the addresses of its
+// entry points.
+#include <Python.h>
+
+#include <ATen/ATen.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include "../../../include/fo_ops.h"
+
+namespace {
+
+decltype(&fo_mx4_quantize) quantize_entry;
+decltype(&fo_mx4_dequantize) dequantize_entry;
+decltype(&fo_mx4_gemm) gemm_entry;
+PyObject *error_type;  // called with a status and the entry point's name
+
+// The tensor in `o`, or null: exact tensors alone, whose methods nobody has replaced.
+const at::Tensor *tensor(PyObject *o) { return THPVariable_CheckExact(o) ? &THPVariable_Unpack(o) : nullptr; }
+
+bool ready(const at::Tensor *t, at::ScalarType type, int64_t device) {
+  return t && t->layout() == at::kStrided && t->is_cuda() && t->get_device() == device && t->scalar_type() == type &&
+         t->is_contiguous();
+}
+bool scales_of(const at::Tensor &t, int64_t rows, int64_t blocks) {
+  return t.dim() == 3 && t.size(0) == (blocks + 7) / 8 && t.size(1) == rows && t.size(2) == 8;
+}
+
+// FO_BF16, FO_FP16, FO_FP32
+const at::ScalarType kTypes[] = {at::kBFloat16, at::kHalf, at::kFloat};
+
+PyObject *refused(int rc, const char *what) {
+  if (PyObject *e = PyObject_CallFunction(error_type, "is", rc, what)) {
+    PyErr_SetObject(error_type, e);
+    Py_DECREF(e);
+  }
+  return nullptr;
+}
+
+// Runs f, turning C++ exceptions into Python's.
+template <typename F>
+PyObject *guarded(F f) {
+  try {
+    return f();
+  } catch (const std::exception &e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+    return nullptr;
+  }
+}
+bool integers(PyObject *const *args, int n, int64_t *out) {
+  for (int i = 0; i < n; ++i) {
+    out[i] = PyLong_AsLongLong(args[i]);
+    if (out[i] == -1 && PyErr_Occurred()) return false;
+  }
+  return true;
+}
+hipStream_t stream_of(int64_t address) { return reinterpret_cast<hipStream_t>(static_cast<intptr_t>(address)); }
+
+// quantize(x, device, stream) -> (codes, scales)
+PyObject *quantize(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  int64_t v[2];
+  if (n != 3 || !integers(args + 1, 2, v)) return PyErr_Occurred() ? nullptr : refused(FO_ERR_INVALID, "quantize");
+  return guarded([&]() -> PyObject * {
+    const at::Tensor *x = tensor(args[0]);
+    if (!x || x->layout() != at::kStrided || !x->is_cuda() || x->get_device() != v[0] || x->dim() != 2) Py_RETURN_NONE;
+    const at::ScalarType type = x->scalar_type();
+    if (type != at::kBFloat16 && type != at::kHalf) Py_RETURN_NONE;
+    const int64_t rows = x->size(0), cols = x->size(1), ld = rows > 1 ? x->stride(0) : cols;
+    if (cols < 1 || ld < cols || (cols > 1 && x->stride(1) != 1)) Py_RETURN_NONE;
+    const int64_t blocks = (cols + 31) / 32;
+    const auto bytes = at::TensorOptions(at::kByte).device(x->device());
+    at::Tensor codes = at::empty({rows, 16 * blocks}, bytes);
+    at::Tensor scales = at::empty({(blocks + 7) / 8, rows, 8}, bytes);
+    const int rc = quantize_entry(x->data_ptr(), rows, cols, ld, type == at::kBFloat16 ? FO_BF16 : FO_FP16,
+                                  codes.data_ptr(), scales.data_ptr(), stream_of(v[1]));
+    if (rc != FO_OK) return refused(rc, "fo_mx4_quantize");
+    PyObject *const c = THPVariable_Wrap(std::move(codes)), *const s = c ? THPVariable_Wrap(std::move(scales)) : nullptr;
+    PyObject *const both = s ? PyTuple_Pack(2, c, s) : nullptr;
+    Py_XDECREF(c);
+    Py_XDECREF(s);
+    return both;
+  });
+}
+
+// dequantize(codes, scales, cols, type, device, stream) -> out
+PyObject *dequantize(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  int64_t v[4];
+  if (n != 6 || !integers(args + 2, 4, v)) return PyErr_Occurred() ? nullptr : refused(FO_ERR_INVALID, "dequantize");
+  return guarded([&]() -> PyObject * {
+    const at::Tensor *codes = tensor(args[0]), *scales = tensor(args[1]);
+    const int64_t cols = v[0], type = v[1], device = v[2];
+    if (!ready(codes, at::kByte, device) || !ready(scales, at::kByte, device) || cols < 1 || codes->dim() != 2 ||
+        type < FO_BF16 || type > FO_FP32)
+      Py_RETURN_NONE;
+    const int64_t rows = codes->size(0), blocks = codes->size(1) / 16;
+    if (codes->size(1) % 16 || blocks != (cols - 1) / 32 + 1 || !scales_of(*scales, rows, blocks)) Py_RETURN_NONE;
+    at::Tensor out = at::empty({rows, cols}, at::TensorOptions(kTypes[type]).device(codes->device()));
+    const int rc = dequantize_entry(codes->data_ptr(), scales->data_ptr(), rows, cols, (int32_t)type, out.data_ptr(),
+                                    stream_of(v[3]));
+    return rc == FO_OK ? THPVariable_Wrap(std::move(out)) : refused(rc, "fo_mx4_dequantize");
+  });
+}
+
+// gemm(a_codes, a_scales, b_codes, b_scales, row_ends or None, type, device, stream) -> out
+PyObject *gemm(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  int64_t v[3];
+  if (n != 8 || !integers(args + 5, 3, v)) return PyErr_Occurred() ? nullptr : refused(FO_ERR_INVALID, "gemm");
+  return guarded([&]() -> PyObject * {
+    const at::Tensor *t[4];
+    for (int i = 0; i < 4; ++i) {
+      t[i] = tensor(args[i]);
+      if (!ready(t[i], at::kByte, v[1])) Py_RETURN_NONE;
+    }
+    if (t[0]->dim() != 2 || t[2]->dim() != 2 || v[0] < FO_BF16 || v[0] > FO_FP16) Py_RETURN_NONE;
+    const int64_t rows = t[0]->size(0), rows_b = t[2]->size(0), row = t[0]->size(1), blocks = row / 16;
+    if (t[2]->size(1) != row || row % 16 || !scales_of(*t[1], rows, blocks) || !scales_of(*t[3], rows_b, blocks))
+      Py_RETURN_NONE;
+    int64_t problems = 1;
+    const int32_t *ends = nullptr;
+    if (args[4] != Py_None) {
+      const at::Tensor *e = tensor(args[4]);
+      if (!ready(e, at::kInt, v[1]) || e->dim() != 1 || e->numel() < 1 || e->numel() > INT32_MAX) Py_RETURN_NONE;
+      problems = e->numel();
+      ends = e->data_ptr<int32_t>();
+    }
+    if (rows_b % problems) Py_RETURN_NONE;
+    const int64_t N = rows_b / problems;
+    at::Tensor out = at::empty({rows, N}, at::TensorOptions(kTypes[v[0]]).device(t[0]->device()));
+    const int rc = gemm_entry(t[0]->data_ptr(), t[1]->data_ptr(), t[2]->data_ptr(), t[3]->data_ptr(), out.data_ptr(),
+                              rows, N, 32 * blocks, (int32_t)v[0], (int32_t)problems, ends, stream_of(v[2]));
+    return rc == FO_OK ? THPVariable_Wrap(std::move(out)) : refused(rc, "fo_mx4_gemm");
+  });
+}
+
+// bind(quantize's address, dequantize's, gemm's, the error's type)
+PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  int64_t v[3];
+  if (n != 4 || !integers(args, 3, v)) {
+    if (!PyErr_Occurred()) PyErr_SetString(PyExc_TypeError, "bind: three addresses and the error's type");
+    return nullptr;
+  }
+  quantize_entry = reinterpret_cast<decltype(quantize_entry)>(v[0]);
+  dequantize_entry = reinterpret_cast<decltype(dequantize_entry)>(v[1]);
+  gemm_entry = reinterpret_cast<decltype(gemm_entry)>(v[2]);
+  Py_INCREF(args[3]);
+  Py_XDECREF(error_type);
+  error_type = args[3];
+  Py_RETURN_NONE;
+}
+
+template <typename F>
+PyMethodDef entry(const char *name, F f) {
+  return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr};
+}
+PyMethodDef methods[] = {entry("bind", &bind), entry("quantize", &quantize), entry("dequantize", &dequantize),
+                         entry("gemm", &gemm), {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", "The 4-bit operators' ordinary calls.", -1, methods,
+                      nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__calls() { return PyModule_Create(&module); }
