@@ -1,4 +1,5 @@
 // Product of two 4-bit (MX) operands: out = A . B^T, sums in fp32.
+#include <algorithm>
 #include <type_traits>
 
 #include "../ops_internal.h"
@@ -95,18 +96,18 @@ constexpr uint32_t kOutOfRange = 0xC0000000u;  // a byte offset past every buffe
 template <int BM, int BN, int NW, int NS_>
 struct Cfg {
   static constexpr int THREADS = 64 * NW, NS = NS_;
-  static constexpr int WGM = 2, WGN = NW / 2;
+  static constexpr int WGM = BM > BN ? NW / 2 : 2, WGN = NW / WGM;
   static constexpr int WM = BM / WGM, WN = BN / WGN, FM = WM / 32, FN = WN / 32;
   static constexpr int ROWB = 128, CHUNKS = 8, KS = 4;   // a slice is 4 k-steps of 64 values
   static constexpr int A_PER_T = BM * CHUNKS / THREADS, B_PER_T = BN * CHUNKS / THREADS;
-  // scale bytes of a slice: 8 a row, loaded 4 a lane: 2 BM + 2 BN lanes
-  static constexpr int S_PER_T = (2 * BM + 2 * BN) / THREADS;
+  // scale bytes of a slice: 8 a row, loaded 4 a lane: 2 BM + 2 BN lanes, rounded up to whole workgroups
+  static constexpr int S_PER_T = (2 * BM + 2 * BN + THREADS - 1) / THREADS;
   static constexpr int LOADS = A_PER_T + B_PER_T + S_PER_T;
   // Of a slice's loads, those issued beside the last k-step of the slice that frees its
   // stage; the rest follow a k-step later (all of them at once hold the wave up: 2 - 7%
   // slower on 256 x 256 tiles).
   static constexpr int EARLY = LOADS / 3;
-  static constexpr int B_AT = BM * ROWB, S_AT = (BM + BN) * ROWB, STAGE = S_AT + (BM + BN) * 8;
+  static constexpr int B_AT = BM * ROWB, S_AT = (BM + BN) * ROWB, STAGE = S_AT + S_PER_T * THREADS * 4;
   static constexpr int OUT_PITCH = 80;                   // a wave's 32 x 32 block: 64 bytes a row, padded
   static constexpr int OUT_AT = NS * STAGE, LDS = OUT_AT + NW * 32 * OUT_PITCH;
   static constexpr int STORES = FM * FN * 2;
@@ -186,6 +187,7 @@ __global__ __launch_bounds__(64 * NW, 2) void mx4_gemm_tiled(Mx4Params p) {
         constexpr int qs = q - C::A_PER_T - C::B_PER_T;
         const int piece = qs * NW + wave;
         const bool is_a = C::S_PER_T == 2 ? qs == 0 : wave < BM / 32;
+        // a piece past B's rows reads zeros, as rows past `cols` do
         const __amdgpu_buffer_rsrc_t rs = is_a ? make_rsrc(sa0, rows * 8) : make_rsrc(sb0, cols * 8);
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(dst + C::S_AT + piece * 256), 4,
                                                  (uint32_t)((is_a ? piece : piece - BM / 32) * 256 + lane * 4), 0, 0, 0);
@@ -500,18 +502,26 @@ int launch_any(const Mx4Params &p, int cus, hipStream_t s) {
   }
   // Otherwise the tile with the least time: rounds of tiles over the CUs, at the
   // microseconds a slice that each tile was measured to take with one (c1) and two
-  // (c2) workgroups on a CU: 0.40 and 0.57 for 64 x 64, 0.92 and 1.44 for 128 x 128,
-  // 2.15 for 256 x 256, of which one fits.  (777 x 4104 x 2752: 18.5, 14.1 and 23.9 us;
-  // 512 x 4096 x 4096: 11.9, 17.9, 28.8; 1024 x 8192 x 8192: 77, 48, 62; 2048 rows: 159, 88, 68.)
-  auto time = [&](int64_t bm, double c1, double c2, int slots) {
-    const int64_t tiles = ((p.M + bm - 1) / bm + (p.problems - 1) / 2) * ((p.N + bm - 1) / bm);
+  // (c2) workgroups on a CU, or alone where it fills the CU's LDS.  Two stages and two
+  // workgroups a CU are ahead where there are tiles for both; with one round of tiles
+  // eight waves and four stages are (128 x 128, one round / two: 1024 x 4096 x 4096
+  // 15.5 / 18.9 us, 1024 x 8192 x 8192 48.0 / 43.5).  (64 x 64, 128 x 64, the better
+  // 128 x 128 and 256 x 256: 512 x 4096 x 4096 12.6, 11.4, 13.8, 28.8 us;
+  // 256 x 8192 x 8192 21.8, 18.5, 23.4, 54; 777 x 4104 x 2752 20.5, 20.0, 14.5, 24.9;
+  // 2048 x 8192 x 8192 150, -, 83.6, 65.4; cold operands.)
+  auto time = [&](int64_t bm, int64_t bn, double c1, double c2, int slots) {
+    const int64_t tiles = ((p.M + bm - 1) / bm + (p.problems - 1) / 2) * ((p.N + bn - 1) / bn);
     const int64_t full = tiles / (slots * cus), left = tiles % (slots * cus);
     return full * c2 + (left == 0 ? 0.0 : left <= cus ? c1 : c2);
   };
-  const double t64 = time(64, 0.40, 0.57, 2), t128 = time(128, 0.92, 1.44, 2), t256 = time(256, 2.15, 2.15, 1);
-  if (t256 <= t128 && t256 <= t64) return launch_tiled<T, 256, 256, 8, 2>(p, cus, s);
-  if (t128 <= t64) return launch_tiled<T, 128, 128, 4, 2>(p, cus, s);
-  return launch_tiled<T, 64, 64, 4, 4>(p, cus, s);
+  const double t64 = time(64, 64, 0.40, 0.57, 2), t128x64 = time(128, 64, 0.54, 0.54, 1);
+  const double t128 = time(128, 128, 0.92, 1.44, 2), t128_deep = time(128, 128, 0.75, 0.75, 1);
+  const double t256 = time(256, 256, 2.15, 2.15, 1), least = std::min({t64, t128x64, t128, t128_deep, t256});
+  if (t256 == least) return launch_tiled<T, 256, 256, 8, 2>(p, cus, s);
+  if (t128 == least) return launch_tiled<T, 128, 128, 4, 2>(p, cus, s);
+  if (t128_deep == least) return launch_tiled<T, 128, 128, 8, 4>(p, cus, s);
+  if (t64 == least) return launch_tiled<T, 64, 64, 4, 4>(p, cus, s);
+  return launch_tiled<T, 128, 64, 8, 4>(p, cus, s);
 }
 
 }  // namespace
