@@ -44,7 +44,7 @@ struct MoeParams {
   uint16_t *x_panels;  // [tokens][1 or 2][panels of D]: the tokens as 4-bit weights meet them
   uint16_t *h;         // [rows][2][F, or panels of F]
   float *partial;      // [splits][T][D]
-  int32_t T, D, F, E, top_k, first, local, renorm, expert_wgs, tiles, most, splits;
+  int32_t T, D, F, E, top_k, first, local, renorm, expert_wgs, k_wgs, tiles, most, splits;
 };
 
 template <typename T>
@@ -150,7 +150,8 @@ __device__ __forceinline__ bool arrive_last(uint32_t *counter, uint32_t of) {
   return last;
 }
 
-// Picks of one token by one wave; expert e is in lane e % 64, register e / 64.
+// Picks of one token by one wave; expert e is in lane e % 64, register e / 64;
+// logit(e) is 0 from the number of experts on.
 // Lane j < top_k returns pick j and its weight.
 template <int R, typename Load>
 __device__ __forceinline__ void select_token(const MoeParams &p, int lane, Load &&logit, int *id, float *weight) {
@@ -159,7 +160,7 @@ __device__ __forceinline__ void select_token(const MoeParams &p, int lane, Load 
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int e = i * 64 + lane;
-    l[i] = e < p.E ? logit(e) : 0.0f;
+    l[i] = logit(e);
     key[i] = e < p.E ? order_key(l[i]) : 0u;
   }
   float top = 0, sum = 0, picked = 0, w = 0;
@@ -198,8 +199,8 @@ __device__ __forceinline__ void select_token(const MoeParams &p, int lane, Load 
   *weight = w / (p.renorm ? picked : sum);
 }
 
-// Router.  A workgroup multiplies 16 experts with 16 tokens, its 16 waves each a
-// share of the hidden size.  The last workgroup of a token tile picks for its
+// Router.  A workgroup multiplies 16 experts with 16 tokens over a share of the
+// hidden size, split once more over its 16 waves.  The last workgroup of a token tile picks for its
 // tokens, a wave each; the last tile lists the active experts.
 constexpr int kRouterWaves = 16;
 template <typename T>
@@ -212,7 +213,7 @@ __global__ __launch_bounds__(64 * kRouterWaves) void moe_router(MoeParams p) {
   __shared__ int32_t row_of[kMaxExperts];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
   constexpr int kThreads = 64 * kRouterWaves;
-  const int wgs = p.expert_wgs * p.tiles;
+  const int per_tile = p.expert_wgs * p.k_wgs, wgs = per_tile * p.tiles;
   if ((int)blockIdx.x >= wgs) {  // the workgroups that lay the tokens out for 4-bit weights
     constexpr bool PAIR = std::is_same_v<T, _Float16>;
     const int chunks = p.D / 8, n = p.T * chunks, step = (gridDim.x - wgs) * kThreads;
@@ -238,7 +239,8 @@ __global__ __launch_bounds__(64 * kRouterWaves) void moe_router(MoeParams p) {
     }
     return;
   }
-  const int tile = blockIdx.x / p.expert_wgs, e0 = (blockIdx.x % p.expert_wgs) * 16, t0 = tile * 16;
+  const int tile = blockIdx.x / per_tile, in = blockIdx.x - tile * per_tile, part = in / p.expert_wgs;
+  const int e0 = (in - part * p.expert_wgs) * 16, t0 = tile * 16;
   const int rows_e = min(16, p.E - e0), rows_t = min(16, p.T - t0);
   {
     const uint32_t pitch = (uint32_t)p.D * 2u;
@@ -246,13 +248,13 @@ __global__ __launch_bounds__(64 * kRouterWaves) void moe_router(MoeParams p) {
     const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.x + (int64_t)t0 * p.D, rows_t * pitch);
     f32x4 acc = {};
     constexpr int U = 8;
-    const int steps = (p.D + 31) / 32;
-    for (int s = wave; s < steps; s += kRouterWaves * U) {
+    const int all = (p.D + 31) / 32, steps = all * (part + 1) / p.k_wgs;
+    for (int s = all * part / p.k_wgs + wave; s < steps; s += kRouterWaves * U) {
       u32x4 a[U], b[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int k = (s + u * kRouterWaves) * 32 + g * 8;
-        const uint32_t at = k < p.D ? r * pitch + k * 2u : kOutOfRange;
+        const int su = s + u * kRouterWaves, k = su * 32 + g * 8;
+        const uint32_t at = su < steps && k < p.D ? r * pitch + k * 2u : kOutOfRange;
         a[u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ra, at, 0, 0));
         b[u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rb, at, 0, 0));
       }
@@ -269,10 +271,10 @@ __global__ __launch_bounds__(64 * kRouterWaves) void moe_router(MoeParams p) {
 #pragma unroll
     for (int w = 0; w < kRouterWaves; ++w) s += red[w][l][q];
     tile_logits[t][e] = s;
-    if (p.expert_wgs > 1 && t < rows_t && e < rows_e) put(&p.logits[(int64_t)(t0 + t) * p.E + e0 + e], s);
+    if (per_tile > 1 && t < rows_t && e < rows_e) put(&p.logits[((int64_t)part * p.T + t0 + t) * p.E + e0 + e], s);
   }
-  if (p.expert_wgs > 1) {
-    if (!arrive_last(&p.counters[1 + tile], p.expert_wgs)) return;
+  if (per_tile > 1) {
+    if (!arrive_last(&p.counters[1 + tile], per_tile)) return;
   } else {
     __syncthreads();
   }
@@ -280,9 +282,19 @@ __global__ __launch_bounds__(64 * kRouterWaves) void moe_router(MoeParams p) {
     const int t = t0 + wave;
     int id = 0;
     float w = 0;
-    auto far = [&](int e) { return get(&p.logits[(int64_t)t * p.E + e]); };
-    if (p.expert_wgs == 1)
-      select_token<1>(p, lane, [&](int e) { return tile_logits[wave][e]; }, &id, &w);
+    // the parts' sums, in order; what is not there reads as zero, so that all loads start together
+    const __amdgpu_buffer_rsrc_t rl = make_rsrc(p.logits, (uint32_t)(p.k_wgs * p.T * p.E) * 4u);
+    auto far = [&](int e) {
+      float l = 0;
+#pragma unroll
+      for (int q = 0; q < kRouterMaxParts; ++q) {
+        const uint32_t at = q < p.k_wgs && e < p.E ? (uint32_t)((q * p.T + t) * p.E + e) * 4u : kOutOfRange;
+        l += __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rl, at, 0, kCoherent));
+      }
+      return l;
+    };
+    if (per_tile == 1)
+      select_token<1>(p, lane, [&](int e) { return e < p.E ? tile_logits[wave][e] : 0.0f; }, &id, &w);
     else if (p.E <= 64)
       select_token<1>(p, lane, far, &id, &w);
     else if (p.E <= 128)
@@ -1015,10 +1027,21 @@ template <typename T, bool MX4, int RBU, int CTU>
 int launch_first(const MoeParams &p, hipStream_t s) {
   // workgroups that lay the tokens out: 8 values a thread
   const int lay = MX4 ? (p.T * (p.D / 8) + 64 * kRouterWaves - 1) / (64 * kRouterWaves) : 0;
-  moe_router<T><<<p.expert_wgs * p.tiles + lay, 64 * kRouterWaves, 0, s>>>(p);
+  moe_router<T><<<p.expert_wgs * p.k_wgs * p.tiles + lay, 64 * kRouterWaves, 0, s>>>(p);
   if (hipGetLastError() != hipSuccess) return FO_ERR_HIP;
   moe_up<T, MX4, RBU, CTU><<<dim3((p.F + 16 * RBU - 1) / (16 * RBU), p.most), 64 * kUpWaves, 0, s>>>(p);
   return hipGetLastError() == hipSuccess ? FO_OK : FO_ERR_HIP;
+}
+
+// Workgroups that share the hidden size of a router tile.  One CU brings about 40 bytes
+// a nanosecond, so a tile's rows are most of the router's time; a join costs 1 us, which
+// is paid anyway where several workgroups share the experts.  (Router with and without:
+// 16 tokens on 8 experts, hidden 4096, 8.6 and 10.1 us; 64 on 64, 2048: 10.6 and 12.5;
+// one token on 8 stays whole: 6.9.)
+int router_parts(const MoeParams &p) {
+  const int64_t bytes = (int64_t)((p.E < 16 ? p.E : 16) + (p.T < 16 ? p.T : 16)) * p.D * 2;
+  const int64_t parts = p.expert_wgs > 1 ? bytes / (32 << 10) : bytes < (128 << 10) ? 1 : bytes / (48 << 10);
+  return parts < 1 ? 1 : parts > kRouterMaxParts ? kRouterMaxParts : (int)parts;
 }
 
 // Workgroups that share a tile of outputs: one for every CU, as long as each has `least` units of work.
@@ -1123,6 +1146,7 @@ int launch_moe(const fo_moe_desc &d, int32_t tokens, const void *x, const void *
   p.renorm = d.renormalize;
   p.expert_wgs = (d.experts + 15) / 16;
   p.tiles = (tokens + 15) / 16;
+  p.k_wgs = router_parts(p);
   p.most = p.local < p.T * p.top_k ? p.local : p.T * p.top_k;  // experts that can be active
   if (d.weights == FO_MOE_MX4)
     return d.dtype == FO_BF16 ? launch_typed<__bf16, true>(p, cus, s) : launch_typed<_Float16, true>(p, cus, s);

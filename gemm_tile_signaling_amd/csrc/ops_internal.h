@@ -17,8 +17,8 @@ int launch_mx4_gemm(const void *a_codes, const void *a_scales, const void *b_cod
                     int64_t M, int64_t N, int64_t K, int32_t dtype, int32_t problems, const int32_t *row_ends,
                     int cus, hipStream_t s);
 
-// Most workgroups that share one tile of a layer's outputs.
-constexpr int kMoeMaxSplits = 32;
+// Most workgroups that share one tile of a layer's outputs, and the hidden size of one tile of its router.
+constexpr int kMoeMaxSplits = 32, kRouterMaxParts = 4;
 
 // Parts of a layer's workspace, as byte offsets; each begins on 256 bytes.
 struct MoeLayout {
@@ -28,7 +28,7 @@ struct MoeLayout {
   int64_t row_w;     // float [max_tokens * top_k]: weight of each row of h
   int64_t ids;       // int32 [max_tokens][top_k]: picked experts
   int64_t wts;       // float [max_tokens][top_k]: their weights
-  int64_t logits;    // float [max_tokens][experts]
+  int64_t logits;    // float [kRouterMaxParts][max_tokens][experts]
   int64_t x_panels;  // bf16 [max_tokens][1, or 2 for fp16][hidden, whole panels]: the tokens (4-bit weights only)
   int64_t h;         // 16-bit [max_tokens * top_k][2][ffn, whole panels with 4-bit weights]: the activations as pairs
   int64_t partial;   // float [kMoeMaxSplits][max_tokens][hidden]
@@ -51,7 +51,7 @@ inline MoeLayout moe_layout(const fo_moe_desc &d) {
   l.row_w = take(4 * picks);
   l.ids = take(4 * picks);
   l.wts = take(4 * picks);
-  l.logits = take(4 * (int64_t)d.max_tokens * d.experts);
+  l.logits = take(4 * (int64_t)kRouterMaxParts * d.max_tokens * d.experts);
   l.x_panels = take(mx4 ? 2 * (d.dtype == FO_FP16 ? 2 : 1) * d.max_tokens * whole(d.hidden) : 0);
   l.h = take(4 * picks * (mx4 ? whole(d.ffn) : d.ffn));
   l.partial = take(4 * (int64_t)kMoeMaxSplits * d.max_tokens * d.hidden);
