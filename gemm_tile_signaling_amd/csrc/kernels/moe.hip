@@ -555,6 +555,10 @@ __device__ __forceinline__ void fold(f32x4 (&acc)[NA][CT]) {
 }
 
 // Up: 16 RB values of h per workgroup for one active expert; the waves split the hidden size.
+// Bound by the weights' bytes: 8 experts of 4096 x 14336, one token (2 of them) in 16 bits 79 us,
+// 5.95 TB/s; 16 tokens in 4 bits 98 us, 5.0 TB/s.  With 4-bit weights a wave's share is 4 panels,
+// and each begins with a trip to memory; three waves a SIMD (98 -> 105 us), two waves a workgroup
+// (105), 16 values a workgroup (115) and two panels under way (110) were slower.
 constexpr int kUpWaves = 4;
 template <typename T, bool MX4, int RB, int CTMAX>
 __global__ __launch_bounds__(64 * kUpWaves, 2) void moe_up(MoeParams p) {
@@ -680,7 +684,8 @@ __device__ __forceinline__ void join_parts(const MoeParams &p, int d0) {
 // h comes as pairs of 16-bit values, [row][2][F] (F in panels with 4-bit weights).
 // DENSE (at most 8 tokens): columns t and t + 8 are token t; otherwise an
 // expert's tokens are packed into as few tiles as hold them, and the results
-// moved to the tokens' places (TT tiles of 16 tokens).
+// moved to the tokens' places (TT tiles of 16 tokens).  Bound by the weights' bytes
+// where they are many: 2 experts of 4096 x 14336 in 16 bits 42 us, 5.6 TB/s.
 constexpr int kDownWaves = 8;
 template <typename T, bool MX4, int RB, bool DENSE, int TT>
 __global__ __launch_bounds__(64 * kDownWaves, 2) void moe_down(MoeParams p) {
@@ -812,7 +817,9 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void moe_down(MoeParams p) {
 // split the rows instead, 16 RB each, and share a stage of h in LDS: KU values of
 // every column of the expert at hand.  Stage and weights of the next unit are
 // loaded while a unit is multiplied, one barrier a unit.  The workgroups of a
-// row tile share the active experts' ffn evenly as in moe_down.
+// row tile share the active experts' ffn evenly as in moe_down.  (16 tokens on 8
+// experts of 4096 x 14336 in 4 bits 61 us, 4.0 TB/s; 64 tokens on 8 of 2048 x 768 24 us,
+// of which counting the parts takes 1.4 and adding them up 5.)
 constexpr int kWideWaves = 8;
 template <bool MX4>
 struct DownWide {
@@ -1044,9 +1051,11 @@ int router_parts(const MoeParams &p) {
   return parts < 1 ? 1 : parts > kRouterMaxParts ? kRouterMaxParts : (int)parts;
 }
 
-// Workgroups that share a tile of outputs: one for every CU, as long as each has `least` units of work.
+// Workgroups that share a tile of outputs: as many as make one round of workgroups on the
+// CUs (one more each: 30 experts of 928 x 3200 in 4 bits 34.6 us instead of 23.5, 290
+// workgroups instead of 232), as long as each has `least` units of work.
 int splits_of(const MoeParams &p, int cus, int tiles, int64_t units, int64_t least) {
-  int64_t splits = (cus + tiles - 1) / tiles;
+  int64_t splits = cus / tiles;
   if (splits > p.most * units / least) splits = p.most * units / least;
   if (splits > kMoeMaxSplits) splits = kMoeMaxSplits;
   return splits < 1 ? 1 : (int)splits;
@@ -1085,28 +1094,40 @@ int launch_down_wide(MoeParams p, int cus, hipStream_t s) {
 // (own / shared, us): 16-bit, 64 tokens on 8 experts of 4096 x 14336 737 / 205, on 125
 // of 2048 x 768 179 / 90, 13 tokens on 71 of them 47 / 53; 4-bit, 16 tokens on 8 of 4096 x
 // 14336 98 / 62, 64 tokens on 126 of 2048 x 768 47 / 61, on 8 of 2048 x 1408 12 / 23.
-// The first product takes 32 values of h a workgroup instead of 16 with 4-bit weights
-// from 2^27 values on (126 of 2048 x 768: 60 -> 50 us; 8 of 2048 x 1408: 13.7 -> 14.4).
+// With 4-bit weights a wave that takes more rows asks for the tokens' values less often: the
+// first product takes 32 values of h a workgroup instead of 16 from 2^27 values on (126 of
+// 2048 x 768: 60 -> 50 us, 8 tokens on 7 of 4096 x 14336 96 -> 85; 8 of 2048 x 1408: 13.7 ->
+// 14.4), the second 32 outputs from 2^26 on (24 tokens on 59 of 2048 x 1408 33 -> 27 us, one
+// on 2 of 4096 x 14336 19.6 -> 18.0; 6 of 2048 x 1408: 7.0 -> 8.2) and, for at most 8 tokens,
+// 64 from 2^28 on (8 on 7 of 4096 x 14336: 64, 56 and 49 us).
 template <typename T, bool MX4>
 int launch_typed(const MoeParams &p, int cus, hipStream_t s) {
   constexpr int X = MX4 && std::is_same_v<T, _Float16> ? 2 : 1;  // columns of a token in the first product
+  constexpr int R2 = MX4 ? 2 : 1, R4 = MX4 ? 4 : 1;              // row blocks of many 4-bit weights
   const int64_t values = (int64_t)p.most * p.D * p.F;
-  const bool big = MX4 && values >= (1ll << 27);
+  const bool up2 = MX4 && values >= (1ll << 27), down2 = MX4 && values >= (1ll << 26), down4 = MX4 && values >= (1ll << 28);
   const bool shared = (int64_t)p.T * p.top_k >= 3ll * p.E && (!MX4 || values >= (1ll << 28));
   if (p.T <= 8) {
-    if (const int rc = launch_first<T, MX4, 1, X>(p, s)) return rc;
-    return launch_down<T, MX4, 1, true, 1>(p, cus, s);
+    if (const int rc = up2 ? launch_first<T, MX4, R2, X>(p, s) : launch_first<T, MX4, 1, X>(p, s)) return rc;
+    return down4 ? launch_down<T, MX4, R4, true, 1>(p, cus, s)
+           : down2 ? launch_down<T, MX4, R2, true, 1>(p, cus, s) : launch_down<T, MX4, 1, true, 1>(p, cus, s);
   }
+  auto down = [&](auto ttc) {
+    constexpr int TT = decltype(ttc)::value;
+    return shared ? launch_down_wide<T, MX4, TT>(p, cus, s)
+           : down2 ? launch_down<T, MX4, R2, false, TT>(p, cus, s) : launch_down<T, MX4, 1, false, TT>(p, cus, s);
+  };
+  using std::integral_constant;
   if (p.T <= 16) {
-    if (const int rc = big ? launch_first<T, MX4, 2, X>(p, s) : launch_first<T, MX4, 1, X>(p, s)) return rc;
-    return shared ? launch_down_wide<T, MX4, 1>(p, cus, s) : launch_down<T, MX4, 1, false, 1>(p, cus, s);
+    if (const int rc = up2 ? launch_first<T, MX4, R2, X>(p, s) : launch_first<T, MX4, 1, X>(p, s)) return rc;
+    return down(integral_constant<int, 1>{});
   }
   if (p.T <= 32) {
-    if (const int rc = big ? launch_first<T, MX4, 2, 2 * X>(p, s) : launch_first<T, MX4, 1, 2 * X>(p, s)) return rc;
-    return shared ? launch_down_wide<T, MX4, 2>(p, cus, s) : launch_down<T, MX4, 1, false, 2>(p, cus, s);
+    if (const int rc = up2 ? launch_first<T, MX4, R2, 2 * X>(p, s) : launch_first<T, MX4, 1, 2 * X>(p, s)) return rc;
+    return down(integral_constant<int, 2>{});
   }
-  if (const int rc = big ? launch_first<T, MX4, 2, 4>(p, s) : launch_first<T, MX4, 1, 4>(p, s)) return rc;
-  return shared ? launch_down_wide<T, MX4, 4>(p, cus, s) : launch_down<T, MX4, 1, false, 4>(p, cus, s);
+  if (const int rc = up2 ? launch_first<T, MX4, R2, 4>(p, s) : launch_first<T, MX4, 1, 4>(p, s)) return rc;
+  return down(integral_constant<int, 4>{});
 }
 
 }  // namespace

@@ -1,4 +1,17 @@
-// Product of two 4-bit (MX) operands: out = A . B^T, sums in fp32.
+// Product of two 4-bit (MX) operands: out = A . B^T, sums in fp32, rounded once.
+//
+// out[m][n] = sum over blocks b of 2^(sa[m][b] - 127) 2^(sb[n][b] - 127) sum over the
+// block's 32 values of qa qb.  The scaled matrix instructions do all of it: each lane
+// gives one row's codes of a block and its scale byte, which the layout of the scales
+// (8 blocks of a row together) puts into one register for a slice's k-steps.
+//
+// Few rows of A: B's bytes bound it, mx4_gemm_few streams them to registers (1 x 8192 x
+// 3584: 5.5 us; 1 x 14336 x 8192: 15 us, 4.2 TB/s).  Otherwise mx4_gemm_tiled:
+//   2048 x 8192 x 8192 on normal values  60 us, 4.6 PFLOP/s; 8192 x 14336 x 4096 over 8
+//   problems 262 us, 3.7.  The matrix pipe is 51% busy at 1.81 GHz: power bounds it, and
+//   v_mfma_scale_f32_32x32x64 alone reaches 6.2 PFLOP/s on such values.
+//   One round of tiles (777 x 4104 x 2752: 12.3 us, 128 x 8192 x 3584: 7.1 us) is bound by
+//   a slice's chain of barrier, LDS reads and products, 0.35 us and more.
 #include <algorithm>
 #include <type_traits>
 
@@ -91,6 +104,15 @@ __device__ __forceinline__ void static_for(F &&f) {
 
 constexpr uint32_t kOutOfRange = 0xC0000000u;  // a byte offset past every buffer resource made here
 
+// Operands go to LDS by loads that write it directly: the wait for a stage is a count of
+// the wave's own loads, and a slice costs one barrier.  The next tile's first slices are
+// loaded before this tile's results are stored.  What was slower (us before -> after):
+// slices of 128 values in four stages (2048 x 8192 x 8192, 72 -> 83: half lines, twice the
+// requests), lines touched two slices ahead (72 -> 75), v_mfma_scale_f32_16x16x128 in the
+// 256 x 256 tile (66 -> 71, no room for its fragments), two whole slices' fragments in
+// registers (128 x 8192 x 3584 8.7 -> 9.3, 1024 x 8192 x 8192 43.6 -> 46.9), eight stages
+// (64 x 8192 x 8192 14.7 -> 15.5).
+//
 // Tile BM x BN; K-slices of 256 values (128 bytes of codes a row, 8 blocks) in
 // a ring of NS LDS stages; NW waves in a WGM x WGN grid.
 template <int BM, int BN, int NW, int NS_>
