@@ -556,8 +556,8 @@ __device__ __forceinline__ void fold(f32x4 (&acc)[NA][CT]) {
 
 // Up: 16 RB values of h per workgroup for one active expert; the waves split the hidden size.
 // Bound by the weights' bytes: 8 experts of 4096 x 14336, one token (2 of them) in 16 bits 79 us,
-// 5.95 TB/s; 16 tokens in 4 bits 98 us, 5.0 TB/s.  With 4-bit weights a wave's share is 4 panels,
-// and each begins with a trip to memory; three waves a SIMD (98 -> 105 us), two waves a workgroup
+// 5.95 TB/s; 16 tokens in 4 bits 98 us, 5.0 TB/s (rows of 2 KB, 128 bytes of each at a time:
+// loads alone in this order reach 5.5).  With 4-bit weights three waves a SIMD (98 -> 105 us), two waves a workgroup
 // (105), 16 values a workgroup (115) and two panels under way (110) were slower.
 constexpr int kUpWaves = 4;
 template <typename T, bool MX4, int RB, int CTMAX>
@@ -1093,7 +1093,8 @@ int launch_down_wide(MoeParams p, int cus, hipStream_t s) {
 // there is enough to read (2^28 values) to make up for its fewer, longer parts.  Measured
 // (own / shared, us): 16-bit, 64 tokens on 8 experts of 4096 x 14336 737 / 205, on 125
 // of 2048 x 768 179 / 90, 13 tokens on 71 of them 47 / 53; 4-bit, 16 tokens on 8 of 4096 x
-// 14336 98 / 62, 64 tokens on 126 of 2048 x 768 47 / 61, on 8 of 2048 x 1408 12 / 23.
+// 14336 77 / 62, 64 tokens 151 / 86, on 126 of 2048 x 768 40 / 61, on 8 of 2048 x 1408 12 / 23,
+// on 16 of them (16 tokens an expert) 33 / 36.
 // With 4-bit weights a wave that takes more rows asks for the tokens' values less often: the
 // first product takes 32 values of h a workgroup instead of 16 from 2^27 values on (126 of
 // 2048 x 768: 60 -> 50 us, 8 tokens on 7 of 4096 x 14336 96 -> 85; 8 of 2048 x 1408: 13.7 ->
