@@ -557,8 +557,9 @@ __device__ __forceinline__ void fold(f32x4 (&acc)[NA][CT]) {
 // Up: 16 RB values of h per workgroup for one active expert; the waves split the hidden size.
 // Bound by the weights' bytes: 8 experts of 4096 x 14336, one token (2 of them) in 16 bits 79 us,
 // 5.95 TB/s; 16 tokens in 4 bits 98 us, 5.0 TB/s (rows of 2 KB, 128 bytes of each at a time:
-// loads alone in this order reach 5.5).  With 4-bit weights three waves a SIMD (98 -> 105 us), two waves a workgroup
-// (105), 16 values a workgroup (115) and two panels under way (110) were slower.
+// loads alone in this order reach 5.5).  With 4-bit weights three waves a SIMD (98 -> 105 us),
+// two waves a workgroup (105), 16 values a workgroup (115) and two panels under way (110)
+// were slower.
 constexpr int kUpWaves = 4;
 template <typename T, bool MX4, int RB, int CTMAX>
 __global__ __launch_bounds__(64 * kUpWaves, 2) void moe_up(MoeParams p) {
